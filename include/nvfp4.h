@@ -14,6 +14,9 @@
  *     rebuilt to bf16 for windowed attention (hyper.ai LongLive-2.0 summary,
  *     section "方法" (Method), second paragraph), over a window of 9 local plus
  *     3 sink frames (171host.com LongLive 2.0 teardown, section 2.2).
+ *   - For single tokens and batches of requests: matrix-vector products with the NVFP4
+ *     weights, and a paged 8-bit KV cache (page plans, the quantizing write, ragged
+ *     attention).  The pages have no counterpart.
  *   - Around them: the FFN's GELU in the GEMM epilogue, windowed attention that
  *     reads the NVFP4 cache directly, and host-side slot planning under the
  *     two-level (global and per-shot) attention sinks of multi-shot generation
@@ -71,7 +74,8 @@ typedef enum {
   NVFP4_ERR_ARCH = 5,              /* current device is not sm_100 */
   NVFP4_ERR_CUDA = 6,              /* a CUDA runtime call or launch failed */
   NVFP4_ERR_TIMEOUT = 7,           /* device: a bounded wait ran out */
-  NVFP4_ERR_DOMAIN = 8             /* device: tensor scale outside the domain */
+  NVFP4_ERR_DOMAIN = 8,            /* device: tensor scale outside the domain */
+  NVFP4_ERR_CAPACITY = 9           /* device: pages, table or slot map too small */
 } nvfp4_status;
 
 /* Element type of a dense input or output tensor. */
@@ -319,6 +323,149 @@ NVFP4_API nvfp4_status nvfp4_sink_plan_next(nvfp4_sink_plan* plan, int32_t n_fra
                                             int32_t new_shot, int32_t* dst_slots,
                                             int32_t* window_slots, int32_t* n_window);
 NVFP4_API int64_t nvfp4_sink_plan_frame_of_slot(const nvfp4_sink_plan* plan, int32_t slot);
+
+/* Matrix-vector products with NVFP4 weights: the linear layer of a few rows, whose
+ * activations are not quantized,
+ *   y[m][n] = act(s_t * sum_k x[m][k] v(q[n][k]) s_b[n][k/16])
+ * Products are exact up to the representation of x (below), sums fp32.
+ *   x:   device, bf16 or fp32 (x_dtype), m rows of W->cols values at stride ldx
+ *        elements, 1 <= m <= NVFP4_GEMV_MAX_ROWS; 16-byte aligned, ldx * element size
+ *        a multiple of 16 bytes.  Each row is taken, per 128 columns, relative to the
+ *        largest magnitude there: bf16 values exactly down to 2^-22 of it and within
+ *        2^-33 of it below; fp32 values within 2^-22 relative, or 2^-43 of it below.
+ *   W:   N x K weights, either scale layout; K a multiple of 32.
+ *   y:   device, bf16 or fp32 (y_dtype), row stride ldy >= N elements.
+ *   act: nvfp4_act.  The GELU takes y rounded to bf16 for bf16 output, and uses the
+ *        exact tanh to fp32 accuracy (not the approximation of nvfp4_gemm).
+ * No workspace; the result does not depend on timing.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, ARCH, CUDA. */
+#define NVFP4_GEMV_MAX_ROWS 16
+NVFP4_API nvfp4_status nvfp4_gemv(const void* x, int32_t x_dtype, int64_t m, int64_t ldx,
+                                  const nvfp4_tensor* W, void* y, int32_t y_dtype, int64_t ldy,
+                                  int32_t act, void* stream);
+
+/* Block tables and slot maps of a paged cache, from request lengths, on the device.
+ * For request b with c = cached_lens[b] tokens in the cache and t = new_lens[b] to come:
+ *   - pages ceil(c / P) .. ceil((c + t) / P) - 1 of its table row are taken from
+ *     free_pages, request after request, from index free_head[0] on;
+ *   - token i of the new ones (cu_new[b] + i in the packed order) gets the slot
+ *     page * P + (c + i) % P, page the table's entry (c + i) / P;
+ *   - seq_lens[b] = c + t, cu_new = the exclusive sums of t and their total,
+ *     free_head_out = free_head + pages taken, slot_map = -1 past the last new token.
+ * All or nothing: where the pages, a table row or the slot map are too small
+ * (NVFP4_ERR_CAPACITY in the status word), or a length is negative or free_head outside
+ * [0, n_free] (NVFP4_ERR_INVALID_ARG), the tables stay as they are, seq_lens =
+ * cached_lens, cu_new = 0, slot_map = -1 and free_head_out = free_head.  A page id
+ * outside [0, n_pages) gives slots of -1 and records INVALID_ARG.
+ *   cached_lens, new_lens: device [batch], 0 <= batch <= NVFP4_PLAN_MAX_BATCH.
+ *   block_table: device [batch][table_stride], max_pages <= table_stride entries used.
+ *   free_pages: device [n_free]; free_head, free_head_out: device [1].
+ *   seq_lens [batch], cu_new [batch + 1], slot_map [max_new]: device, written whole; the
+ *   outputs are buffers of their own, none of them an input.
+ *   page_tokens: a multiple of 16 up to NVFP4_KV8_MAX_PAGE_TOKENS; n_pages * page_tokens
+ *   and max_pages * page_tokens below 2^31.
+ *   ws: device workspace (status word).
+ * Finished requests give pages back by the caller's writing them before free_head.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+#define NVFP4_PLAN_MAX_BATCH 8192
+#define NVFP4_KV8_MAX_PAGE_TOKENS 4096
+NVFP4_API nvfp4_status nvfp4_plan_pages(const int32_t* cached_lens, const int32_t* new_lens,
+                                        int32_t batch, int32_t* block_table, int64_t table_stride,
+                                        int32_t max_pages, const int32_t* free_pages,
+                                        int32_t n_free, const int32_t* free_head,
+                                        int32_t page_tokens, int32_t n_pages, int32_t* seq_lens,
+                                        int32_t* cu_new, int32_t* slot_map, int32_t max_new,
+                                        int32_t* free_head_out, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* The paged 8-bit KV cache of one layer: E4M3 codes and one scale for each page (block
+ * of page_tokens tokens of one request) and head, value = code * scale.
+ *   k_codes, v_codes: device [n_pages][kv_heads][page_tokens][head_dim] bytes
+ *   k_scale, v_scale: device [n_pages][kv_heads] floats, powers of two in [2^-60, 2^60]
+ * Codes 16-byte aligned; head_dim 64 or 128; page_tokens a multiple of 16 up to
+ * NVFP4_KV8_MAX_PAGE_TOKENS; n_pages * page_tokens < 2^31. */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t kv_heads;
+  int32_t head_dim;
+} nvfp4_kv8_cache;
+
+#define NVFP4_KV8_MIN_EXP (-60)
+#define NVFP4_KV8_MAX_EXP 60
+#define NVFP4_KV8_MAX_SPLITS 128
+
+/* Write new tokens into the cache.  The new tokens of one page and head get the scale
+ *   s = 2^e, e the smallest in [-60, 60] with max|x| <= 448 * 2^e,
+ * or the page's present scale where that is larger and the page already holds tokens
+ * (its first new slot is not its first slot); where the scale grows, the page's tokens
+ * before the first new one are coded again.  code = E4M3_RNE_sat(x / s).
+ *   k, v: device bf16, tokens rows at token_stride elements (a multiple of 8, >= kv_heads
+ *         * head_dim), kv_heads x head_dim contiguous in a row; 16-byte aligned.
+ *   slot_map: device [tokens], page * page_tokens + place in the page; -1 skips a token.
+ *         The new tokens of one page are neighbours in it, in ascending order without
+ *         gaps (as nvfp4_plan_pages gives them), and every slot appears once: else the
+ *         contents of the pages concerned are unspecified.
+ *   ws:   device workspace.
+ * A slot outside the cache is skipped and records NVFP4_ERR_INVALID_ARG.  Non-finite
+ * values record NVFP4_ERR_DOMAIN: they do not count for the scale, infinities are stored
+ * as the largest code and NaN as 0, so that no code is ever NaN.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, ARCH, CUDA. */
+NVFP4_API nvfp4_status nvfp4_kv8_append(const nvfp4_kv8_cache* cache, const void* k, const void* v,
+                                        int64_t token_stride, int64_t tokens,
+                                        const int32_t* slot_map, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* The queries and the cached tokens of a batch of requests.
+ *   cu_q:        device [batch + 1], request b has the queries cu_q[b] .. cu_q[b+1] - 1
+ *   kv_lens:     device [batch], tokens in the cache (its new ones included)
+ *   block_table: device [batch][table_stride], max_pages entries used a row
+ *   max_q:       host, no request has more queries
+ *   max_kv:      host, about the largest kv_lens: how the work is split goes by it, the
+ *                result holds for any value >= 1 */
+typedef struct {
+  const int32_t* cu_q;
+  const int32_t* kv_lens;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int32_t batch;
+  int32_t max_pages;
+  int32_t max_q;
+  int32_t max_kv;
+} nvfp4_kv8_batch;
+
+/* Attention over the 8-bit cache, single tokens or chunks, ragged:
+ *   out[t][h] = sum_j softmax_j(softmax_scale q[t][h] . k[j]) v[j]
+ * over the tokens j of t's request, K and V head h / (q_heads / kv_heads).  causal != 0:
+ * the queries are the request's last tokens, query i sees the first kv_len - n + 1 + i.
+ * A row that sees nothing is 0 and its log-sum-exp -inf.  Scores, sums and the
+ * normaliser in fp32; probabilities enter the product with V in 16 bits.
+ *   q:   device bf16, tq tokens at q_token_stride elements (>= q_heads * head_dim, a
+ *        multiple of 8), q_heads x head_dim contiguous in a token; 16-byte aligned.
+ *   q_heads: a multiple of kv_heads.
+ *   out: device bf16, same layout at out_token_stride.  Rows of no request are left.
+ *   lse: NULL, or device floats [tq][q_heads]: the natural log-sum-exp of a row's scores.
+ *   scratch: device, nvfp4_kv8_attention_scratch_bytes(...) bytes, 16-byte aligned (NULL
+ *        where that is 0); free for other use once the call's work is done.
+ *   ws:  device workspace (status word).
+ * Lengths and offsets outside the buffers are cut to them and page ids outside the cache
+ * leave their tokens out; both record NVFP4_ERR_INVALID_ARG.
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, WORKSPACE, ARCH, CUDA; TIMEOUT via
+ * the status word. */
+NVFP4_API size_t nvfp4_kv8_attention_scratch_bytes(const nvfp4_kv8_cache* cache,
+                                                   const nvfp4_kv8_batch* batch, int64_t tq,
+                                                   int32_t q_heads, int32_t causal);
+NVFP4_API nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache,
+                                           const nvfp4_kv8_batch* batch, const void* q,
+                                           int64_t q_token_stride, int64_t tq, int32_t q_heads,
+                                           int32_t causal, float softmax_scale, void* out,
+                                           int64_t out_token_stride, float* lse, void* scratch,
+                                           size_t scratch_bytes, void* ws, size_t ws_bytes,
+                                           void* stream);
 
 /* Size of the library-owned scratch array behind nvfp4_quantize_noalloc. */
 #define NVFP4_NOALLOC_SCRATCH_BYTES 256

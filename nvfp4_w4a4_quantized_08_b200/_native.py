@@ -22,6 +22,7 @@ ERR_ARCH = 5
 ERR_CUDA = 6
 ERR_TIMEOUT = 7
 ERR_DOMAIN = 8
+ERR_CAPACITY = 9
 
 BF16 = 0
 FP32 = 1
@@ -33,6 +34,9 @@ ACT_NONE = 0
 ACT_GELU_TANH = 1
 KV_MAX_CHUNK_FRAMES = 8
 KV_MAX_WINDOW_SLOTS = 256
+GEMV_MAX_ROWS = 16
+PLAN_MAX_BATCH = 8192
+KV8_MAX_PAGE_TOKENS = 4096
 
 EXPORTS = (
     "nvfp4_codes_bytes", "nvfp4_sf_bytes", "nvfp4_workspace_bytes", "nvfp4_quantize",
@@ -40,6 +44,8 @@ EXPORTS = (
     "nvfp4_get_device_status", "nvfp4_set_wait_limit_ns", "nvfp4_status_string",
     "nvfp4_quantize_noalloc", "nvfp4_window_attention", "nvfp4_sink_plan_create",
     "nvfp4_sink_plan_destroy", "nvfp4_sink_plan_next", "nvfp4_sink_plan_frame_of_slot",
+    "nvfp4_gemv", "nvfp4_plan_pages", "nvfp4_kv8_append", "nvfp4_kv8_attention_scratch_bytes",
+    "nvfp4_kv8_attention",
 )
 
 
@@ -55,6 +61,20 @@ class KvCache(ctypes.Structure):
                 ("n_slots", ctypes.c_int32), ("tokens_per_frame", ctypes.c_int32),
                 ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("scale_rule", ctypes.c_int32)]
+
+
+class Kv8Cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class Kv8Batch(ctypes.Structure):
+    _fields_ = [("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("batch", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
 
 
 class NVFP4Error(RuntimeError):
@@ -110,6 +130,19 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_window_attention.argtypes = [KP, ctypes.POINTER(ctypes.c_int32), i32, vp, i64,
                                              i64, ctypes.c_float, vp, i64, vp, ctypes.c_size_t,
                                              vp]
+        L.nvfp4_gemv.restype = i32
+        L.nvfp4_gemv.argtypes = [vp, i32, i64, i64, TP, vp, i32, i64, i32, vp]
+        L.nvfp4_plan_pages.restype = i32
+        L.nvfp4_plan_pages.argtypes = [vp, vp, i32, vp, i64, i32, vp, i32, vp, i32, i32, vp, vp,
+                                       vp, i32, vp, vp, sz, vp]
+        CP, BP = ctypes.POINTER(Kv8Cache), ctypes.POINTER(Kv8Batch)
+        L.nvfp4_kv8_append.restype = i32
+        L.nvfp4_kv8_append.argtypes = [CP, vp, vp, i64, i64, vp, vp, sz, vp]
+        L.nvfp4_kv8_attention_scratch_bytes.restype = sz
+        L.nvfp4_kv8_attention_scratch_bytes.argtypes = [CP, BP, i64, i32, i32]
+        L.nvfp4_kv8_attention.restype = i32
+        L.nvfp4_kv8_attention.argtypes = [CP, BP, vp, i64, i64, i32, i32, ctypes.c_float, vp, i64,
+                                          vp, vp, sz, vp, sz, vp]
         L.nvfp4_get_device_status.restype = i32
         L.nvfp4_get_device_status.argtypes = [vp, vp]
         L.nvfp4_set_wait_limit_ns.restype = None

@@ -71,6 +71,70 @@ nvfp4_status check_cache(const nvfp4_kv_cache* c) {
   return NVFP4_OK;
 }
 
+bool valid_pages(int64_t n_pages, int64_t page_tokens) {
+  return page_tokens % 16 == 0 && page_tokens <= NVFP4_KV8_MAX_PAGE_TOKENS &&
+         n_pages * page_tokens < (int64_t(1) << 31);
+}
+
+nvfp4_status check_kv8(const nvfp4_kv8_cache* c) {
+  if (!c || !c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale) return NVFP4_ERR_INVALID_ARG;
+  if (c->n_pages <= 0 || c->page_tokens <= 0 || c->kv_heads <= 0 || c->head_dim <= 0)
+    return NVFP4_ERR_INVALID_ARG;
+  if ((c->head_dim != 64 && c->head_dim != 128) || c->kv_heads > 65535 ||
+      !valid_pages(c->n_pages, c->page_tokens))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scale, 4) ||
+      !aligned(c->v_scale, 4))
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+// The batch, and the sizes every kernel of the attention relies on.
+nvfp4_status check_kv8_batch(const nvfp4_kv8_cache* c, const nvfp4_kv8_batch* b, int64_t tq,
+                             int32_t q_heads, int32_t causal) {
+  if (!b || !b->cu_q || !b->kv_lens || !b->block_table) return NVFP4_ERR_INVALID_ARG;
+  if (b->batch < 1 || b->max_pages < 1 || b->max_q < 1 || b->max_kv < 1 ||
+      b->table_stride < b->max_pages || tq < 0 || q_heads < 1 || (causal != 0 && causal != 1))
+    return NVFP4_ERR_INVALID_ARG;
+  if (q_heads % c->kv_heads != 0) return NVFP4_ERR_INVALID_ARG;
+  if (b->batch > 65535 || tq * q_heads >= (int64_t(1) << 31) ||
+      int64_t(b->max_q) * q_heads >= (int64_t(1) << 31) ||
+      int64_t(b->max_pages) * c->page_tokens >= (int64_t(1) << 31))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(b->cu_q, 4) || !aligned(b->kv_lens, 4) || !aligned(b->block_table, 4))
+    return NVFP4_ERR_MISALIGNED;
+  return NVFP4_OK;
+}
+
+LaunchKv8Attn kv8_args(const nvfp4_kv8_cache* c, const nvfp4_kv8_batch* b, int64_t tq,
+                       int32_t q_heads, int32_t causal, int sm_count) {
+  LaunchKv8Attn d = {};
+  d.k_codes = c->k_codes;
+  d.v_codes = c->v_codes;
+  d.k_scale = c->k_scale;
+  d.v_scale = c->v_scale;
+  d.n_pages = c->n_pages;
+  d.page_tokens = c->page_tokens;
+  d.kv_heads = c->kv_heads;
+  d.head_dim = c->head_dim;
+  d.tq = tq;
+  d.q_heads = q_heads;
+  d.cu_q = b->cu_q;
+  d.kv_lens = b->kv_lens;
+  d.table = b->block_table;
+  d.table_stride = b->table_stride;
+  d.batch = b->batch;
+  d.max_pages = b->max_pages;
+  // bounds beyond what the buffers hold would only make the grid larger
+  d.max_q = int32_t(b->max_q < tq ? b->max_q : tq);
+  if (d.max_q < 1) d.max_q = 1;
+  const int64_t room = int64_t(b->max_pages) * c->page_tokens;
+  d.max_kv = int32_t(b->max_kv < room ? b->max_kv : room);
+  d.causal = causal;
+  d.sm_count = sm_count;
+  return d;
+}
+
 }  // namespace
 
 extern "C" {
@@ -103,6 +167,7 @@ const char* nvfp4_status_string(nvfp4_status s) {
     case NVFP4_ERR_CUDA: return "CUDA error";
     case NVFP4_ERR_TIMEOUT: return "device wait timed out";
     case NVFP4_ERR_DOMAIN: return "tensor scale outside the recipe's domain";
+    case NVFP4_ERR_CAPACITY: return "page pool, block table or slot map too small";
   }
   return "unknown status";
 }
@@ -330,6 +395,185 @@ nvfp4_status nvfp4_window_attention(const nvfp4_kv_cache* cache, const int32_t* 
   d.ws = ws;
   d.wait_limit_ns = g_wait_limit_ns.load();
   return cuda_status(launch_window_attention(d, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_gemv(const void* x, int32_t x_dtype, int64_t m, int64_t ldx,
+                        const nvfp4_tensor* W, void* y, int32_t y_dtype, int64_t ldy, int32_t act,
+                        void* stream) {
+  nvfp4_status st = check_tensor(W);
+  if (st != NVFP4_OK) return st;
+  if (!x || !y || (x_dtype != NVFP4_BF16 && x_dtype != NVFP4_FP32) ||
+      (y_dtype != NVFP4_BF16 && y_dtype != NVFP4_FP32))
+    return NVFP4_ERR_INVALID_ARG;
+  if (act != NVFP4_ACT_NONE && act != NVFP4_ACT_GELU_TANH) return NVFP4_ERR_INVALID_ARG;
+  if (m < 1 || ldx < W->cols || ldy < W->rows) return NVFP4_ERR_INVALID_ARG;
+  if (m > NVFP4_GEMV_MAX_ROWS || W->cols % 32 != 0 || W->rows >= (int64_t(1) << 30) ||
+      W->cols >= (int64_t(1) << 30))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t xsz = x_dtype == NVFP4_BF16 ? 2 : 4, ysz = y_dtype == NVFP4_BF16 ? 2 : 4;
+  if (!aligned(x, 16) || (ldx * xsz) % 16 != 0 || !aligned(y, uintptr_t(ysz)))
+    return NVFP4_ERR_MISALIGNED;
+  const DeviceInfo dev = current_device();
+  if (!dev.ok) return NVFP4_ERR_ARCH;
+  LaunchGemv g;
+  g.x = x;
+  g.x_dtype = x_dtype;
+  g.M = m;
+  g.N = W->rows;
+  g.K = W->cols;
+  g.ldx = ldx;
+  g.w_codes = W->codes;
+  g.w_sf = W->sf;
+  g.w_st = W->s_t;
+  g.sf_layout = W->sf_layout;
+  g.y = y;
+  g.y_dtype = y_dtype;
+  g.ldy = ldy;
+  g.act = act;
+  g.sm_count = dev.sm_count;
+  return cuda_status(launch_gemv(g, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_plan_pages(const int32_t* cached_lens, const int32_t* new_lens, int32_t batch,
+                              int32_t* block_table, int64_t table_stride, int32_t max_pages,
+                              const int32_t* free_pages, int32_t n_free, const int32_t* free_head,
+                              int32_t page_tokens, int32_t n_pages, int32_t* seq_lens,
+                              int32_t* cu_new, int32_t* slot_map, int32_t max_new,
+                              int32_t* free_head_out, void* ws, size_t ws_bytes, void* stream) {
+  if (batch < 0 || max_pages < 0 || table_stride < max_pages || n_free < 0 || n_pages < 1 ||
+      page_tokens < 1 || max_new < 0)
+    return NVFP4_ERR_INVALID_ARG;
+  if (!free_head || !free_head_out || !cu_new || (n_free > 0 && !free_pages) ||
+      (max_new > 0 && !slot_map))
+    return NVFP4_ERR_INVALID_ARG;
+  if (batch > 0 && (!cached_lens || !new_lens || !seq_lens || (max_pages > 0 && !block_table)))
+    return NVFP4_ERR_INVALID_ARG;
+  if (batch > NVFP4_PLAN_MAX_BATCH || !valid_pages(n_pages, page_tokens) ||
+      int64_t(max_pages) * page_tokens >= (int64_t(1) << 31))
+    return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  const void* ptrs[] = {cached_lens, new_lens, block_table, free_pages, free_head,
+                        seq_lens,    cu_new,   slot_map,    free_head_out};
+  for (const void* p : ptrs)
+    if (!aligned(p, 4)) return NVFP4_ERR_MISALIGNED;
+  // an output that is also read (or written twice) would race between the CTAs
+  struct Span {
+    const int32_t* p;
+    int64_t n;
+  };
+  const int64_t table = batch > 0 && max_pages > 0 ? (batch - 1) * table_stride + max_pages : 0;
+  const Span spans[] = {{cached_lens, batch}, {new_lens, batch},      {free_pages, n_free},
+                        {free_head, 1},       {block_table, table},   {seq_lens, batch},
+                        {cu_new, batch + 1},  {slot_map, max_new},    {free_head_out, 1}};
+  for (int i = 4; i < 9; ++i)
+    for (int j = 0; j < i; ++j)
+      if (spans[i].n > 0 && spans[j].n > 0 && spans[i].p < spans[j].p + spans[j].n &&
+          spans[j].p < spans[i].p + spans[i].n)
+        return NVFP4_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < kWsBytes) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return NVFP4_ERR_MISALIGNED;
+  const DeviceInfo dev = current_device();
+  if (!dev.ok) return NVFP4_ERR_ARCH;
+  LaunchPlan p;
+  p.cached = cached_lens;
+  p.fresh = new_lens;
+  p.table = block_table;
+  p.table_stride = table_stride;
+  p.free_pages = free_pages;
+  p.free_head = free_head;
+  p.seq_lens = seq_lens;
+  p.cu_new = cu_new;
+  p.slot_map = slot_map;
+  p.free_head_out = free_head_out;
+  p.batch = batch;
+  p.max_pages = max_pages;
+  p.n_free = n_free;
+  p.n_pages = n_pages;
+  p.page_tokens = page_tokens;
+  p.max_new = max_new;
+  p.ws = ws;
+  p.sm_count = dev.sm_count;
+  return cuda_status(launch_plan(p, static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_kv8_append(const nvfp4_kv8_cache* cache, const void* k, const void* v,
+                              int64_t token_stride, int64_t tokens, const int32_t* slot_map,
+                              void* ws, size_t ws_bytes, void* stream) {
+  nvfp4_status st = check_kv8(cache);
+  if (st != NVFP4_OK) return st;
+  if (tokens < 0) return NVFP4_ERR_INVALID_ARG;
+  if (tokens > 0 && (!k || !v || !slot_map)) return NVFP4_ERR_INVALID_ARG;
+  if (token_stride < int64_t(cache->kv_heads) * cache->head_dim) return NVFP4_ERR_INVALID_ARG;
+  if (tokens >= (int64_t(1) << 30)) return NVFP4_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned(k, 16) || !aligned(v, 16) || token_stride % 8 != 0 || !aligned(slot_map, 4))
+    return NVFP4_ERR_MISALIGNED;
+  if (!ws || ws_bytes < kWsBytes) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return NVFP4_ERR_MISALIGNED;
+  const DeviceInfo dev = current_device();
+  if (!dev.ok) return NVFP4_ERR_ARCH;
+  if (tokens == 0) return NVFP4_OK;
+  LaunchKv8Append p;
+  p.k = k;
+  p.v = v;
+  p.token_stride = token_stride;
+  p.tokens = tokens;
+  p.slot_map = slot_map;
+  p.k_codes = cache->k_codes;
+  p.v_codes = cache->v_codes;
+  p.k_scale = cache->k_scale;
+  p.v_scale = cache->v_scale;
+  p.n_pages = cache->n_pages;
+  p.page_tokens = cache->page_tokens;
+  p.heads = cache->kv_heads;
+  p.head_dim = cache->head_dim;
+  p.ws = ws;
+  p.sm_count = dev.sm_count;
+  return cuda_status(launch_kv8_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_kv8_attention_scratch_bytes(const nvfp4_kv8_cache* cache,
+                                         const nvfp4_kv8_batch* batch, int64_t tq, int32_t q_heads,
+                                         int32_t causal) {
+  if (check_kv8(cache) != NVFP4_OK || check_kv8_batch(cache, batch, tq, q_heads, causal) != NVFP4_OK)
+    return 0;
+  const DeviceInfo dev = current_device();
+  if (!dev.ok) return 0;
+  return kv8_plan(kv8_args(cache, batch, tq, q_heads, causal, dev.sm_count)).scratch;
+}
+
+nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_batch* batch,
+                                 const void* q, int64_t q_token_stride, int64_t tq,
+                                 int32_t q_heads, int32_t causal, float softmax_scale, void* out,
+                                 int64_t out_token_stride, float* lse, void* scratch,
+                                 size_t scratch_bytes, void* ws, size_t ws_bytes, void* stream) {
+  nvfp4_status st = check_kv8(cache);
+  if (st != NVFP4_OK) return st;
+  st = check_kv8_batch(cache, batch, tq, q_heads, causal);
+  if (st != NVFP4_OK) return st;
+  if (tq > 0 && (!q || !out)) return NVFP4_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return NVFP4_ERR_INVALID_ARG;
+  const int64_t row = int64_t(q_heads) * cache->head_dim;
+  if (q_token_stride < row || out_token_stride < row) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 != 0 ||
+      out_token_stride % 8 != 0 || !aligned(lse, 4) || !aligned(scratch, 16))
+    return NVFP4_ERR_MISALIGNED;
+  if (!ws || ws_bytes < kWsBytes) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return NVFP4_ERR_MISALIGNED;
+  const DeviceInfo dev = current_device();
+  if (!dev.ok) return NVFP4_ERR_ARCH;
+  if (tq == 0) return NVFP4_OK;
+  LaunchKv8Attn d = kv8_args(cache, batch, tq, q_heads, causal, dev.sm_count);
+  const size_t need = kv8_plan(d).scratch;
+  if (need > 0 && (!scratch || scratch_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  d.q = q;
+  d.q_stride = q_token_stride;
+  d.out = out;
+  d.out_stride = out_token_stride;
+  d.lse = lse;
+  d.scale_log2 = float(double(softmax_scale) * 1.4426950408889634);
+  d.scratch = scratch;
+  d.ws = ws;
+  d.wait_limit_ns = g_wait_limit_ns.load();
+  return cuda_status(launch_kv8_attention(d, static_cast<cudaStream_t>(stream)));
 }
 
 nvfp4_status nvfp4_get_device_status(void* ws, void* stream) {

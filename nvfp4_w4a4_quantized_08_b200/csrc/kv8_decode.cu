@@ -1,0 +1,520 @@
+// kv8_decode.cu -- attention of a few rows per request over the paged 8-bit cache
+// (single tokens and short drafts), and the join of split ranges.
+//
+//   out[t][h] = sum_j softmax_j(scale q[t][h] . k[j]) v[j],  k = codes * page scale
+//
+// Bound by the cache: each K and V byte is read once for the rows of one request
+// that share a KV head (G query heads times the request's queries, packed; tiles of
+// 8 NT rows).  One CTA takes one tile of rows, one KV head and one range of tokens;
+// its four warps take groups of 16 tokens in turn, straight from global memory into
+// registers (2 KB of K and 2 KB of V a group and warp for 128 dims, the next group's
+// loads issued before the current one is computed), with no shared memory on the way:
+//
+//   S^T = K Q^T    m16n8k16, A = 16 tokens of K, B = 8 rows of Q.  The order of the
+//                  dims inside a product is free, so a lane's 32 contiguous bytes of a
+//                  token are its A registers after one hardware conversion (E4M3 ->
+//                  fp16, exact) per two elements.
+//   O^T += V^T P^T m16n8k16, A = 16 dims by 16 tokens of V: a lane loads 16 contiguous
+//                  dims of its four tokens and pairs tokens with byte permutes before
+//                  the conversion.  P^T comes from S^T by an 8x8 transposition in
+//                  registers (movmatrix).
+//
+// fp16 operands: Q is scaled by a power of two per row so that its largest element is
+// in [2^8, 2^9) (exact for elements within 2^-22 of it, below that an error of at most
+// 2^-33 of it); sums are fp32.  The page scale of K is multiplied into the fp32 scores.
+// The page scale of V is an exponent added to the probability's, and the weights
+// 2^(x + log2 s_v) are taken against their own running maximum, apart from the one of
+// the normaliser: so fp16 holds them however far apart the pages' scales lie (2^7 at the
+// maximum; an error of at most 2^-32 of it where they become subnormal).  Both maxima
+// are raised lazily: only a group that exceeds one by 2^8 rescales (one warp vote a
+// group decides).
+//
+// Ranges: with few requests and heads the tokens are split over CTAs; each leaves its
+// normalised rows in fp32 and their log-sum-exp, and a second kernel joins them in
+// order of the range, so results do not depend on timing.
+#include "common.cuh"
+#include "kernels.h"
+#include "kv8_batch.cuh"
+
+namespace nvfp4 {
+namespace kv8 {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr float kLazy = 8.0f;
+constexpr float kBias = 7.0f;   // weights are taken times 2^7: at most 2^15 in fp16
+constexpr float kNegInf = -INFINITY;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four E4M3 bytes -> two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Code words of one lane for one group of 16 tokens, and the group's page scales.
+template <int kDim>
+struct Group {
+  static constexpr int kWords = kDim / 16;  // words of one token's share: K dims / 4 lanes
+  uint32_t k[2][kWords];                    // tokens r and r + 8, dims [dim / 4 * c, ..)
+  uint32_t v[4][kDim / 32];                 // tokens 2c, 2c+1, 2c+8, 2c+9, dims [dim / 8 * r, ..)
+  float ks, vs;
+};
+
+template <int kWords>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[kWords]) {
+  if constexpr (kWords == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = v.x;
+    w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) {
+      const uint4 v = ld_nc_v4(p + 16 * i);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+  }
+}
+
+template <int kDim, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_kernel(const Args a) {
+  constexpr int kSteps = kDim / 16;   // k16 steps of S
+  constexpr int kTiles = kDim / 16;   // m16 tiles of O
+  constexpr int kRows = 8 * NT;
+  __shared__ float so[kWarps][kRows][kDim + 4];
+  __shared__ float sm[kWarps][3][kRows];   // maximum, weights' maximum, sum
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+  const int split = blockIdx.x % a.n_splits, tile = blockIdx.x / a.n_splits;
+  const int h = blockIdx.y, b = blockIdx.z;
+  pdl_wait();
+  pdl_trigger();
+  const Request rq = request(a, b, tid == 0 && blockIdx.x == 0 && h == 0);
+  const int rows = rq.nq * a.group;
+  const int rho0 = tile * kRows;
+  if (rho0 >= rows) return;
+  // this CTA's tokens: its range, up to what the tile's last row sees
+  const int last_row = min(rho0 + kRows, rows) - 1;
+  const int used = splits_of(a, rq.kv);
+  if (split >= used) return;
+  const int t_begin = split * a.chunk;
+  const int t_range = split == used - 1 ? rq.kv : min(rq.kv, t_begin + a.chunk);
+  const int t_end = min(t_range, sees(a, rq, last_row));
+
+  // Q: lane's rows r (one per tile), dims [kDim / 4 * c, ..), as B registers
+  uint32_t qf[NT][kSteps][2];
+  float qs[NT][2];   // softmax scale over Q's power of two, for rows 2c and 2c + 1
+  int vis[NT][2];    // tokens those rows see
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int rho = rho0 + 8 * nt + r;
+    uint32_t w[kDim / 8];
+    const bool live = rho < rows;
+    const uint16_t* src = live ? q_row(a, rq, h, rho, kDim) + c * (kDim / 4) : a.q;
+#pragma unroll
+    for (int i = 0; i < kDim / 32; ++i) {
+      const uint4 v = live ? ld_nc_v4_l1(src + 8 * i) : make_uint4(0, 0, 0, 0);
+      w[4 * i] = v.x;
+      w[4 * i + 1] = v.y;
+      w[4 * i + 2] = v.z;
+      w[4 * i + 3] = v.w;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kDim / 8; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const uint32_t field = min(262u - (top >> 7), 253u);   // 2^e as an exponent field
+    const float up = __uint_as_float(field << 23);
+    const float down = __uint_as_float((254u - field) << 23) * a.scale_log2;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t v = w[2 * ks + i];
+        qf[nt][ks][i] =
+            f16x2_rn(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+      }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      qs[nt][i] = __shfl_sync(0xFFFFFFFFu, down, 4 * (2 * c + i));
+      vis[nt][i] = sees(a, rq, min(rho0 + 8 * nt + 2 * c + i, rows - 1));
+    }
+  }
+  // tokens every row of the tile sees (the first row sees the fewest)
+  const int vis_all = sees(a, rq, rho0);
+
+  float o[NT][kTiles][4], l[NT][2], m[NT][2], mv[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[nt][t][i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) l[nt][i] = 0.0f, m[nt][i] = kNegInf, mv[nt][i] = kNegInf;
+  }
+
+  // page of every group of this warp, 32 groups at a time: lane i holds group i's
+  const int32_t* table = a.table + int64_t(b) * a.table_stride;
+  int pages = 0;
+  auto load_pages = [&](int g0) {
+    const int tok = t_begin + (g0 + lane) * (16 * kWarps) + 16 * warp;
+    pages = tok < t_end ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : 0;
+  };
+  auto load = [&](int gi, Group<kDim>& g) {
+    const int tok = t_begin + gi * (16 * kWarps) + 16 * warp;
+    const int id = __shfl_sync(0xFFFFFFFFu, pages, gi & 31);
+    if (tok >= t_end) return;
+    const bool ok = id >= 0 && id < a.n_pages;
+    const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
+    const int64_t ph = int64_t(ok ? id : 0) * a.kv_heads + h;
+    const int64_t at = (ph * a.page_tokens + in_page) * kDim;
+    const uint8_t* kp = a.k_codes + at + r * kDim + c * (kDim / 4);
+    load_words(kp, g.k[0]);
+    load_words(kp + 8 * kDim, g.k[1]);
+    const uint8_t* vp = a.v_codes + at + 2 * c * kDim + r * (kDim / 8);
+    load_words(vp, g.v[0]);
+    load_words(vp + kDim, g.v[1]);
+    load_words(vp + 8 * kDim, g.v[2]);
+    load_words(vp + 9 * kDim, g.v[3]);
+    // a page that is not one of the pool's is left out, and recorded
+    g.ks = ok ? __ldg(a.k_scale + ph) : kNegInf;
+    g.vs = __ldg(a.v_scale + ph);
+    if (!ok && lane == 0) record_status(a.status, NVFP4_ERR_INVALID_ARG);
+  };
+
+  auto compute = [&](int gi, Group<kDim>& g) {
+    const int tok = t_begin + gi * (16 * kWarps) + 16 * warp;
+    const bool bad = g.ks == kNegInf;
+    // V of tokens past the request's end may be anything, NaN codes included: zero
+    if (bad || tok + 16 > rq.kv) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = tok + 2 * c + (i & 1) + 8 * (i >> 1);
+        if (bad || t >= rq.kv) {
+#pragma unroll
+          for (int j = 0; j < kDim / 32; ++j) g.v[i][j] = 0;
+        }
+      }
+    }
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) {
+      uint32_t a0, a1, a2, a3;
+      e4m3_f16(g.k[0][ks], a0, a2);
+      e4m3_f16(g.k[1][ks], a1, a3);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
+    }
+    // log2 of the V scale, exact for a power of two; -inf for 0 (a page never written)
+    const uint32_t vb = __float_as_uint(g.vs);
+    const float lv = vb < 0x00800000u ? kNegInf
+                                      : float(int(vb >> 23) - 127) +
+                                            __log2f(__uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u));
+    const bool masked = bad || tok + 16 > t_range || tok + 16 > vis_all;
+    bool raise = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float f = qs[nt][i] * g.ks;
+        s[nt][i] *= f;
+        s[nt][2 + i] *= f;
+        if (masked) {
+          const int lim = bad ? 0 : min(vis[nt][i], t_range);
+          if (tok + r >= lim) s[nt][i] = kNegInf;
+          if (tok + r + 8 >= lim) s[nt][2 + i] = kNegInf;
+        }
+        const float top = fmaxf(s[nt][i], s[nt][2 + i]);
+        raise |= top > m[nt][i] + kLazy || top + lv > mv[nt][i] + kLazy;
+      }
+    }
+    if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float top = fmaxf(s[nt][i], s[nt][2 + i]);
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+          const float mn = fmaxf(m[nt][i], top), mvn = fmaxf(mv[nt][i], top + lv);
+          if (mn > m[nt][i]) l[nt][i] *= exp2_approx(m[nt][i] - mn);
+          const float f = mvn > mv[nt][i] ? exp2_approx(mv[nt][i] - mvn) : 1.0f;
+          m[nt][i] = mn;
+          mv[nt][i] = mvn;
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            o[nt][t][i] *= f;
+            o[nt][t][2 + i] *= f;
+          }
+        }
+    }
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float base = m[nt][i] == kNegInf ? 0.0f : m[nt][i];
+        const float basev = mv[nt][i] == kNegInf ? 0.0f : mv[nt][i] - lv - kBias;
+        l[nt][i] += exp2_approx(s[nt][i] - base) + exp2_approx(s[nt][2 + i] - base);
+        w[i] = lv == kNegInf ? 0.0f : exp2_approx(s[nt][i] - basev);
+        w[2 + i] = lv == kNegInf ? 0.0f : exp2_approx(s[nt][2 + i] - basev);
+      }
+      pb[nt][0] = transpose8x8(f16x2_rn(w[0], w[1]));
+      pb[nt][1] = transpose8x8(f16x2_rn(w[2], w[3]));
+    }
+#pragma unroll
+    for (int j = 0; j < kDim / 32; ++j) {
+      // words j of four tokens: dims 4 j .. 4 j + 3 of the lane's, two O tiles
+      const uint32_t x0 = prmt(g.v[0][j], g.v[1][j], 0x5140), x1 = prmt(g.v[0][j], g.v[1][j], 0x7362);
+      const uint32_t y0 = prmt(g.v[2][j], g.v[3][j], 0x5140), y1 = prmt(g.v[2][j], g.v[3][j], 0x7362);
+      uint32_t a0, a1, a2, a3;
+      e4m3_f16(x0, a0, a1);
+      e4m3_f16(y0, a2, a3);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * j], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+      e4m3_f16(x1, a0, a1);
+      e4m3_f16(y1, a2, a3);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma_f16(o[nt][2 * j + 1], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+    }
+  };
+
+  const int n_groups = (max(t_end - t_begin, 0) + 16 * kWarps - 1) / (16 * kWarps);
+  Group<kDim> ga, gb;
+  if (n_groups > 0) {
+    load_pages(0);
+    load(0, ga);
+  }
+  for (int gi = 0; gi < n_groups; gi += 2) {
+    if (gi + 1 < n_groups) load(gi + 1, gb);
+    if (t_begin + gi * (16 * kWarps) + 16 * warp < t_end) compute(gi, ga);
+    if (gi + 1 < n_groups) {
+      if (((gi + 2) & 31) == 0) load_pages(gi + 2);
+      if (gi + 2 < n_groups) load(gi + 2, ga);
+      if (t_begin + (gi + 1) * (16 * kWarps) + 16 * warp < t_end) compute(gi + 1, gb);
+    }
+  }
+
+  // join the four warps: sums of the lanes' tokens, then maxima and rows through
+  // shared memory
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], 4);
+      l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], 8);
+      l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], 16);
+      const int row = 8 * nt + 2 * c + i;
+      if (r == 0) {
+        sm[warp][0][row] = m[nt][i];
+        sm[warp][1][row] = mv[nt][i];
+        sm[warp][2][row] = l[nt][i];
+      }
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        so[warp][row][kDim / 8 * r + 2 * t] = o[nt][t][i];
+        so[warp][row][kDim / 8 * r + 2 * t + 1] = o[nt][t][2 + i];
+      }
+    }
+  __syncthreads();
+  constexpr int kPer = kDim / 16;   // 16 lanes a row
+  for (int row = tid >> 4; row < kRows; row += kThreads / 16) {
+    const int rho = rho0 + row;
+    if (rho >= rows) break;
+    float mt = kNegInf, mvt = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      mt = fmaxf(mt, sm[w][0][row]);
+      mvt = fmaxf(mvt, sm[w][1][row]);
+    }
+    const float base = mt == kNegInf ? 0.0f : mt, basev = mvt == kNegInf ? 0.0f : mvt;
+    float sum = 0.0f, f[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      sum += sm[w][2][row] * exp2_approx(sm[w][0][row] - base);
+      f[w] = exp2_approx(sm[w][1][row] - basev);
+    }
+    // 2^(weights' maximum - maximum) / sum; a row that sees nothing is zero
+    const float norm = sum == 0.0f ? 0.0f : exp2f(basev - kBias - base) / sum;
+    const float lse2 = sum == 0.0f ? kNegInf : base + log2f(sum);
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int d = (tid & 15) * kPer + i;
+      float x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) x = fmaf(so[w][row][d], f[w], x);
+      v[i] = x * norm;
+    }
+    store_row<kPer, kDim>(a, rq, h, rho, split, used, (tid & 15) * kPer, v, lse2, (tid & 15) == 0);
+  }
+}
+
+// Joins the ranges of requests that were split: one warp a row, ranges in order.
+template <int kDim>
+__global__ void __launch_bounds__(kThreads) join_kernel(const Args a) {
+  constexpr int kPer = kDim / 32;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const Request rq = request(a, b, false);
+  const int used = splits_of(a, rq.kv);
+  const int n = int(blockIdx.x) * kWarps + (threadIdx.x >> 5);  // (token, head) of the request
+  if (used <= 1 || n >= rq.nq * a.q_heads) return;
+  const int64_t row = int64_t(rq.q0) * a.q_heads + n;
+  const int64_t plane = int64_t(a.tq) * a.q_heads;
+  float top = kNegInf;
+  for (int s = lane; s < used; s += 32) top = fmaxf(top, a.part_lse[s * plane + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const float base = top == kNegInf ? 0.0f : top;
+  float sum = 0.0f, v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+  for (int s = 0; s < used; ++s) {
+    const float w = exp2f(a.part_lse[s * plane + row] - base);
+    const float* p = a.part_o + (s * plane + row) * kDim + lane * kPer;
+    sum += w;
+    if constexpr (kPer == 4) {
+      const float4 x = *reinterpret_cast<const float4*>(p);
+      v[0] = fmaf(w, x.x, v[0]);
+      v[1] = fmaf(w, x.y, v[1]);
+      v[2] = fmaf(w, x.z, v[2]);
+      v[3] = fmaf(w, x.w, v[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(p);
+      v[0] = fmaf(w, x.x, v[0]);
+      v[1] = fmaf(w, x.y, v[1]);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t tok = rq.q0 + n / a.q_heads;
+  uint16_t* dst = a.out + tok * a.out_stride + int64_t(n % a.q_heads) * kDim + lane * kPer;
+  uint32_t w[kPer / 2];
+#pragma unroll
+  for (int i = 0; i < kPer / 2; ++i) w[i] = bf16x2(v[2 * i] * inv, v[2 * i + 1] * inv);
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (a.lse && lane == 0)
+    a.lse[row] = sum == 0.0f ? kNegInf : (base + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int kDim>
+static cudaError_t launch_dim(const Args& a, const Kv8Plan& p, int32_t batch, int32_t max_q,
+                              cudaStream_t st) {
+  const dim3 grid(unsigned(p.n_splits) * unsigned(p.row_tiles), unsigned(a.kv_heads),
+                  unsigned(batch));
+  cudaError_t e = cudaSuccess;
+  if (p.rows == 8)
+    e = launch_pdl(decode_kernel<kDim, 1>, grid, dim3(kThreads), 0, st, a);
+  else
+    e = launch_pdl(decode_kernel<kDim, 2>, grid, dim3(kThreads), 0, st, a);
+  if (e != cudaSuccess || p.n_splits == 1) return e;
+  const int64_t rows = int64_t(max_q) * a.q_heads;
+  return launch_pdl(join_kernel<kDim>, dim3(unsigned((rows + kWarps - 1) / kWarps), unsigned(batch)),
+                    dim3(kThreads), 0, st, a);
+}
+
+}  // namespace kv8
+
+// How a call is laid out; goes by sizes alone, so that the scratch size and the launch agree.
+Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
+  Kv8Plan p;
+  const int32_t group = d.q_heads / d.kv_heads;
+  const int64_t rows = int64_t(d.max_q) * group;
+  p.rows = rows <= 8 ? 8 : 16;
+  p.row_tiles = int32_t((rows + p.rows - 1) / p.rows);
+  // ranges: enough CTAs for a few on every SM, none shorter than 256 tokens
+  const int64_t units = int64_t(d.batch) * d.kv_heads * p.row_tiles;
+  const int64_t want = (int64_t(d.sm_count) * 8 + units - 1) / units;
+  const int64_t most = (int64_t(d.max_kv) + 255) / 256;
+  int64_t n = want < most ? want : most;
+  if (n < 1) n = 1;
+  if (n > NVFP4_KV8_MAX_SPLITS) n = NVFP4_KV8_MAX_SPLITS;
+  const int64_t chunk = ((int64_t(d.max_kv) + n - 1) / n + 63) / 64 * 64;
+  p.chunk = int32_t(chunk < 64 ? 64 : chunk);
+  p.n_splits = int32_t((int64_t(d.max_kv) + p.chunk - 1) / p.chunk);
+  if (p.n_splits < 1) p.n_splits = 1;
+  p.scratch = p.n_splits == 1 ? 0
+                              : size_t(p.n_splits) * size_t(d.tq) * size_t(d.q_heads) *
+                                    size_t(d.head_dim + 1) * sizeof(float);
+  return p;
+}
+
+cudaError_t launch_kv8_attention(const LaunchKv8Attn& d, cudaStream_t st) {
+  const Kv8Plan p = kv8_plan(d);
+  kv8::Args a;
+  a.q = static_cast<const uint16_t*>(d.q);
+  a.q_stride = d.q_stride;
+  a.out = static_cast<uint16_t*>(d.out);
+  a.out_stride = d.out_stride;
+  a.lse = d.lse;
+  a.cu_q = d.cu_q;
+  a.kv_lens = d.kv_lens;
+  a.table = d.table;
+  a.table_stride = d.table_stride;
+  a.k_codes = d.k_codes;
+  a.v_codes = d.v_codes;
+  a.k_scale = d.k_scale;
+  a.v_scale = d.v_scale;
+  a.tq = int32_t(d.tq);
+  a.q_heads = d.q_heads;
+  a.kv_heads = d.kv_heads;
+  a.group = d.q_heads / d.kv_heads;
+  a.group_div = make_fastdiv(uint32_t(a.group));
+  a.max_q = d.max_q;
+  a.max_tokens = int32_t(int64_t(d.max_pages) * d.page_tokens);
+  a.n_pages = d.n_pages;
+  a.page_tokens = d.page_tokens;
+  a.page_div = make_fastdiv(uint32_t(d.page_tokens));
+  a.causal = d.causal;
+  a.scale_log2 = d.scale_log2;
+  a.chunk = p.chunk;
+  a.n_splits = p.n_splits;
+  a.part_o = static_cast<float*>(d.scratch);
+  a.part_lse = a.part_o + int64_t(p.n_splits) * d.tq * d.q_heads * d.head_dim;
+  a.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d.ws) + kWsStatus);
+  return d.head_dim == 64 ? kv8::launch_dim<64>(a, p, d.batch, d.max_q, st)
+                          : kv8::launch_dim<128>(a, p, d.batch, d.max_q, st);
+}
+
+}  // namespace nvfp4

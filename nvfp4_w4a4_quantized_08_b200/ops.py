@@ -234,6 +234,213 @@ class KVCache:
         return out
 
 
+def _launch(fn, what: str, device: torch.device, *args) -> None:
+    """Calls an entry point on `device`'s current stream, with `device` current."""
+    if device.type != "cuda":
+        raise ValueError(f"{what} takes CUDA tensors")
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status != N.OK:
+        raise NVFP4Error(status, what)
+
+
+def _check_int32(device: torch.device, **tensors: torch.Tensor) -> None:
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or t.device != device:
+            raise ValueError(f"{name} must be an int32 tensor on {device}")
+        if t.dim() != 2 and (t.dim() != 1 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous, of one dimension")
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    """The row stride of a 2-D tensor; torch gives any number for a single row."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def gemv(x: torch.Tensor, w: NVFP4Tensor, out_dtype: torch.dtype = torch.bfloat16,
+         out: Optional[torch.Tensor] = None, act: int = N.ACT_NONE) -> torch.Tensor:
+    """nvfp4_gemv: act(x W^T) for 1 to 16 rows x (bf16 or fp32, unit column
+    stride) that are not quantized, and NVFP4 weights -> [x.rows, w.rows] in
+    bf16 or fp32.  For more rows quantize x and use gemm."""
+    if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != w.cols:
+        raise ValueError(f"gemv expects a 2-D tensor of {w.cols} unit-stride columns")
+    if x.device != w.device:
+        raise ValueError("x and w must be on one device")
+    if out is None:
+        out = torch.empty(x.shape[0], w.rows, dtype=out_dtype, device=x.device)
+    elif (out.dim() != 2 or out.shape[0] != x.shape[0] or out.shape[1] < w.rows or
+          out.stride(1) != 1 or out.device != x.device):
+        raise ValueError(f"out must have {x.shape[0]} rows of at least {w.rows} unit-stride "
+                         f"columns on {x.device}")
+    sw = w.c_struct()
+    _launch(N.lib().nvfp4_gemv, "nvfp4_gemv", x.device, x.data_ptr(), _dtype_code(x), x.shape[0],
+            _row_stride(x), ctypes.byref(sw), out.data_ptr(), _dtype_code(out), _row_stride(out),
+            act)
+    return out
+
+
+@dataclass
+class PagePlan:
+    """What plan_pages gives: int32 device tensors."""
+    seq_lens: torch.Tensor   # [batch] tokens of each request, the new ones included
+    cu_new: torch.Tensor     # [batch + 1] offsets of the requests' new tokens
+    slot_map: torch.Tensor   # [max_new] slot of each new token, -1 past the last
+    free_head: torch.Tensor  # [1] first page of the free list that is still free
+
+
+def plan_pages(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+               free_pages: torch.Tensor, free_head: torch.Tensor, page_tokens: int, n_pages: int,
+               max_new: int, ws: Optional[torch.Tensor] = None) -> PagePlan:
+    """nvfp4_plan_pages: pages and slots for each request's new tokens, on the
+    device.  block_table [batch, max_pages] is updated in place; the rest are
+    new tensors (free_head of the result goes into the next call).  Lengths that
+    do not fit are reported by device_status, and then change nothing."""
+    dev = block_table.device
+    _check_int32(dev, cached_lens=cached_lens, new_lens=new_lens, block_table=block_table,
+                 free_pages=free_pages, free_head=free_head)
+    batch = cached_lens.shape[0]
+    if (block_table.dim() != 2 or block_table.shape[0] != batch or new_lens.shape[0] != batch or
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1) or free_head.numel() != 1):
+        raise ValueError("plan_pages: block_table must be [batch, max_pages] with unit column "
+                         "stride, new_lens [batch], free_head [1]")
+    seq, cu = cached_lens.new_empty(batch), cached_lens.new_empty(batch + 1)
+    slots, head = cached_lens.new_empty(max_new), cached_lens.new_empty(1)
+    ws = workspace(dev) if ws is None else ws
+    _launch(N.lib().nvfp4_plan_pages, "nvfp4_plan_pages", dev, cached_lens.data_ptr(),
+            new_lens.data_ptr(), batch, block_table.data_ptr(),
+            _row_stride(block_table), block_table.shape[1],
+            free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(), page_tokens, n_pages,
+            seq.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new, head.data_ptr(),
+            ws.data_ptr(), ws.numel())
+    return PagePlan(seq, cu, slots, head)
+
+
+class KVCache8:
+    """The paged 8-bit KV cache of one layer: E4M3 codes [n_pages, kv_heads,
+    page_tokens, head_dim] and a power-of-two scale [n_pages, kv_heads] for K and
+    for V.  A page holds page_tokens consecutive tokens of one request; which
+    page is whose is the callers' (plan_pages keeps block tables)."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
+                 v_scale: torch.Tensor):
+        """A cache over buffers of the caller's; see empty() for new ones."""
+        shape, dev = k_codes.shape, k_codes.device
+        if len(shape) != 4 or v_codes.shape != shape:
+            raise ValueError("codes must be [n_pages, kv_heads, page_tokens, head_dim]")
+        for t in (k_codes, v_codes):
+            if t.dtype != torch.float8_e4m3fn or not t.is_contiguous() or t.device != dev:
+                raise ValueError("codes must be contiguous float8_e4m3fn tensors on one device")
+        for t in (k_scale, v_scale):
+            if (t.dtype != torch.float32 or t.shape != shape[:2] or not t.is_contiguous() or
+                    t.device != dev):
+                raise ValueError(f"scales must be contiguous fp32 tensors {tuple(shape[:2])}")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = shape
+
+    @classmethod
+    def empty(cls, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int,
+              device="cuda") -> "KVCache8":
+        codes = [torch.zeros(n_pages, kv_heads, page_tokens, head_dim, dtype=torch.uint8,
+                             device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+        scale = [torch.zeros(n_pages, kv_heads, dtype=torch.float32, device=device)
+                 for _ in range(2)]
+        return cls(*codes, *scale)
+
+    def c_struct(self) -> N.Kv8Cache:
+        return N.Kv8Cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(),
+                          self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.n_pages,
+                          self.page_tokens, self.kv_heads, self.head_dim)
+
+    def _rows(self, name: str, t: torch.Tensor, heads: int) -> int:
+        """The token stride of a bf16 tensor [tokens, heads, head_dim] or [tokens,
+        heads * head_dim] whose tokens are contiguous."""
+        d = self.head_dim
+        if t.dim() == 3:
+            ok = t.shape[1] == heads and t.shape[2] == d and t.stride(2) == 1 and \
+                (heads == 1 or t.stride(1) == d)
+        else:
+            ok = t.dim() == 2 and t.shape[1] == heads * d and t.stride(1) == 1
+        if not ok or t.dtype != torch.bfloat16 or t.device != self.k_codes.device:
+            raise ValueError(f"{name} must be a bf16 tensor [tokens, {heads}, {d}] on "
+                             f"{self.k_codes.device}, contiguous inside a token")
+        return t.stride(0) if t.shape[0] > 1 else heads * d
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
+               ws: Optional[torch.Tensor] = None) -> None:
+        """nvfp4_kv8_append: writes the tokens of k and v (bf16 [tokens,
+        kv_heads, head_dim], views into a fused projection included) to their
+        slots (a plan's slot_map; its first entries, if it is longer)."""
+        stride = self._rows("k", k, self.kv_heads)
+        tokens = k.shape[0]
+        if v.shape[0] != tokens or self._rows("v", v, self.kv_heads) != stride:
+            raise ValueError("k and v must share their tokens and a token stride")
+        _check_int32(k.device, slot_map=slot_map)
+        if slot_map.dim() != 1 or slot_map.shape[0] < tokens:
+            raise ValueError(f"slot_map must have at least {tokens} entries")
+        ws = workspace(k.device) if ws is None else ws
+        cs = self.c_struct()
+        _launch(N.lib().nvfp4_kv8_append, "nvfp4_kv8_append", k.device, ctypes.byref(cs),
+                k.data_ptr(), v.data_ptr(), stride, tokens, slot_map.data_ptr(), ws.data_ptr(),
+                ws.numel())
+
+    def attention(self, q: torch.Tensor, cu_q: torch.Tensor, seq_lens: torch.Tensor,
+                  block_table: torch.Tensor, max_q: Optional[int] = None,
+                  max_kv: Optional[int] = None, causal: bool = True,
+                  scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  return_lse: bool = False, ws: Optional[torch.Tensor] = None):
+        """nvfp4_kv8_attention: softmax(scale q k^T) v of each request's queries
+        over its cached tokens.
+
+        q:         bf16 [tokens, q_heads, head_dim], the requests' queries packed;
+                   q_heads a multiple of kv_heads.
+        cu_q, seq_lens, block_table: int32 [batch + 1], [batch], [batch, pages] (a
+                   plan's cu_new and seq_lens).
+        max_q:     no request has more queries (default: all of q's tokens).
+        max_kv:    about the longest request (default: the table's width); the
+                   split of the work goes by it, not the result.
+        causal:    the queries are the requests' last tokens and see no later one.
+        Returns out [tokens, q_heads, head_dim] in bf16, and with return_lse the
+        fp32 log-sum-exp [tokens, q_heads] too.  Rows of no request are left as
+        they are in `out`."""
+        if q.dim() != 3 or q.shape[2] != self.head_dim:
+            raise ValueError(f"q must be [tokens, q_heads, {self.head_dim}]")
+        tokens, heads = q.shape[0], q.shape[1]
+        stride = self._rows("q", q, heads)
+        dev = q.device
+        _check_int32(dev, cu_q=cu_q, seq_lens=seq_lens, block_table=block_table)
+        batch = seq_lens.shape[0]
+        if (cu_q.dim() != 1 or seq_lens.dim() != 1 or cu_q.shape[0] != batch + 1 or
+                block_table.dim() != 2 or block_table.shape[0] != batch or
+                (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+            raise ValueError("attention: cu_q must be [batch + 1], seq_lens [batch] and "
+                             "block_table [batch, pages] with unit column stride")
+        if out is None:
+            out = torch.empty(tokens, heads, self.head_dim, dtype=torch.bfloat16, device=dev)
+        elif out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+        out_stride = self._rows("out", out, heads)
+        lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev) if return_lse else None
+        pages = block_table.shape[1]
+        cs = self.c_struct()
+        cb = N.Kv8Batch(cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
+                        _row_stride(block_table), batch, pages,
+                        max(tokens, 1) if max_q is None else max_q,
+                        pages * self.page_tokens if max_kv is None else max_kv)
+        ws = workspace(dev) if ws is None else ws
+        need = int(N.lib().nvfp4_kv8_attention_scratch_bytes(
+            ctypes.byref(cs), ctypes.byref(cb), tokens, heads, int(causal)))
+        # a tensor of the call's own: calls on other streams and captured graphs share nothing
+        scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        _launch(N.lib().nvfp4_kv8_attention, "nvfp4_kv8_attention", dev, ctypes.byref(cs),
+                ctypes.byref(cb), q.data_ptr(), stride, tokens, heads, int(causal),
+                self.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
+                out_stride, _ptr(lse), _ptr(scratch), need, ws.data_ptr(), ws.numel())
+        return (out, lse) if return_lse else out
+
+
 class SinkPlan:
     """nvfp4_sink_plan: host-side slot planning under the two-level attention
     sinks (global sinks kept for good, shot sinks re-bound at cuts, a local

@@ -1,0 +1,150 @@
+"""GPU parity: nvfp4_gemv against the 64-bit product with the decoded weights.
+
+Bounds.  S = sum_k |x w|, X = sum_k (largest |x| of the 128 columns around k) |w|:
+  representation of x  bf16: 2^-33 X; fp32: 2^-22 S + 2^-43 X
+  sums                 8 tensor-core products of 16 columns each (truncating, 2^-22 of the running
+                       sum at most) and fp32 additions: (8 2^-22 + 32 2^-24) S = 2^-18.7 S
+so |y - ref| <= 2^-18 S + 2^-32 X + 2^-24 |ref|; bf16 output adds half a step, 2^-8 of the value.
+GELU (slope at most 1.13): 1.13 times the error of its input (for bf16 output with the input's
+own rounding to bf16), 2^-18 |y| for the fp32 evaluation, then the output's rounding."""
+import pytest
+import torch
+
+import nvfp4_w4a4_quantized_08_b200 as nv
+
+from _util import GELU_SLOPE_MAX, sf_rowmajor
+
+pytestmark = pytest.mark.gpu
+
+E2M1 = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, 0, -0.5, -1, -1.5, -2, -3, -4, -6],
+                    dtype=torch.float64)
+
+
+def _weights(orc, n, k, layout, seed):
+    g = torch.Generator().manual_seed(seed)
+    w = (torch.randn(n, k, generator=g) * 0.02).to(torch.bfloat16)
+    q = nv.quantize(w.cuda(), sf_layout=layout)
+    code = q.codes.cpu().int()
+    v = E2M1[torch.stack((code & 15, code >> 4), 2).reshape(n, k).long()]
+    sf = torch.from_numpy(sf_rowmajor(orc, q).copy()).view(torch.float8_e4m3fn).double()
+    return q, v * sf.repeat_interleave(16, 1) * q.s_t.cpu().double()
+
+
+def _check(y, x, w, bf16, gelu=False):
+    x = x.double().cpu()
+    ref = x @ w.t()
+    m, k = x.shape
+    pad = torch.zeros(m, -(-k // 128) * 128, dtype=torch.float64)
+    pad[:, :k] = x.abs()
+    near = pad.view(m, -1, 128).amax(2).repeat_interleave(128, 1)[:, :k]
+    S, X = x.abs() @ w.abs().t(), near @ w.abs().t()
+    tol = 2.0 ** -18 * S + 2.0 ** -32 * X + 2.0 ** -24 * ref.abs()
+    if gelu:
+        if bf16:
+            tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+        tol = GELU_SLOPE_MAX * tol + 2.0 ** -18 * ref.abs()
+        u = (2 / torch.pi) ** 0.5 * (ref + 0.044715 * ref ** 3)
+        ref = 0.5 * ref * (1 + torch.tanh(u))
+    if bf16:
+        tol = tol + 2.0 ** -8 * (ref.abs() + tol)
+    err = (y.double().cpu() - ref).abs()
+    assert bool((err <= tol).all()), (float((err / tol.clamp_min(1e-300)).max()),
+                                      (err > tol).nonzero()[:4].tolist())
+
+
+@pytest.mark.parametrize("m", [1, 2, 3, 4, 5, 8, 9, 16])
+@pytest.mark.parametrize("xd", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,k", [(130, 1056), (1, 32), (257, 128)])
+def test_rows(orc, m, xd, n, k):
+    q, w = _weights(orc, n, k, nv.SF_MMA128x4, n + k)
+    x = torch.randn(m, k, generator=torch.Generator().manual_seed(m)).to(xd).cuda()
+    _check(nv.gemv(x, q), x, w, True)
+    _check(nv.gemv(x, q, torch.float32), x, w, False)
+
+
+@pytest.mark.parametrize("layout", [nv.SF_ROWMAJOR, nv.SF_MMA128x4])
+@pytest.mark.parametrize("n,k", [(1000, 14336), (4100, 2080), (64, 8192)])
+def test_layouts_and_splits(orc, layout, n, k):
+    """Row-major and tensor-core scales; columns split over a cluster and not."""
+    q, w = _weights(orc, n, k, layout, 5)
+    x = torch.randn(3, k, generator=torch.Generator().manual_seed(1)).cuda()
+    _check(nv.gemv(x, q, torch.float32), x, w, False)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("m", [1, 6])
+def test_gelu(orc, bf16, m):
+    q, w = _weights(orc, 300, 512, nv.SF_MMA128x4, 9)
+    x = (torch.randn(m, 512, generator=torch.Generator().manual_seed(2)) * 4).to(torch.bfloat16)
+    y = nv.gemv(x.cuda(), q, torch.bfloat16 if bf16 else torch.float32, act=nv.ACT_GELU_TANH)
+    _check(y, x, w, bf16, gelu=True)
+
+
+@pytest.mark.parametrize("xd", [torch.bfloat16, torch.float32])
+def test_wide_range_of_x(orc, xd):
+    """Outlier columns, zero rows, tiny and huge rows, subnormal bf16 values."""
+    q, w = _weights(orc, 200, 640, nv.SF_MMA128x4, 3)
+    x = torch.randn(6, 640, generator=torch.Generator().manual_seed(4))
+    x[0, 7] = 3e4
+    x[1] = 0
+    x[2] *= 1e-30
+    x[3] *= 1e30
+    x[4, :128] *= 1e-20
+    x[5] *= 2.0 ** -130
+    x = x.to(xd).cuda()
+    y = nv.gemv(x, q, torch.float32)
+    keep = torch.tensor([0, 1, 2, 3, 4])
+    _check(y[keep.cuda()], x[keep.cuda()], w, False)
+    # row 5: sums of 640 products below 2^-126, where fp32 itself has steps of 2^-149
+    ref = x[5:].double().cpu() @ w.t()
+    assert bool(((y[5:].double().cpu() - ref).abs() <= 640 * 2.0 ** -149 + 2.0 ** -18 *
+                 (x[5:].double().cpu().abs() @ w.abs().t())).all())
+    assert not y[1].any()
+
+
+def test_strides_and_out(orc):
+    q, w = _weights(orc, 150, 256, nv.SF_MMA128x4, 8)
+    wide = torch.randn(5, 400, generator=torch.Generator().manual_seed(6)).to(torch.bfloat16).cuda()
+    x = wide[:, 64:64 + 256]
+    out = torch.full((5, 160), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert nv.gemv(x, q, out=out) is out
+    _check(out[:, :150], x, w, True)
+    assert bool((out[:, 150:] == 7).all())
+    one = nv.gemv(wide[2:3, 64:64 + 256], q)
+    _check(one, x[2:3], w, True)
+
+
+def test_matches_itself_graphs_and_streams(orc):
+    """Bitwise the same eagerly, on another stream and in a replayed graph with new inputs."""
+    q, _ = _weights(orc, 1000, 4096, nv.SF_MMA128x4, 2)
+    x = torch.randn(2, 4096, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    x2 = x.flip(1).contiguous()
+    want, want2 = nv.gemv(x, q).clone(), nv.gemv(x2, q).clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = nv.gemv(x, q)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, want)
+    buf = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = nv.gemv(buf, q)
+    buf.copy_(x2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want2)
+
+
+def test_near_gemm_and_oracle(orc):
+    """The same layer through the quantized GEMM and the unquantized product: the GEMM's own
+    oracle of the quantized x bounds how far the two may be apart."""
+    q, w = _weights(orc, 256, 512, nv.SF_MMA128x4, 12)
+    x = torch.randn(4, 512, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    qx = nv.quantize(x)
+    xq = nv.dequantize(qx)
+    # |x - dequantized x| enters the product linearly
+    far = (x.double() - xq.double()).abs().cpu() @ w.abs().t()
+    y, yq = nv.gemv(x, q, torch.float32), nv.gemm(qx, q, torch.float32)
+    S = xq.double().abs().cpu() @ w.abs().t()
+    assert bool(((y - yq).double().abs().cpu() <= far + (2e-3 + 2.0 ** -8) * S).all())

@@ -1,0 +1,220 @@
+"""Host-side refusals of the matrix-vector, page-plan and 8-bit cache entry points: every call
+has an invalid argument, so it returns before any device work."""
+import ctypes
+
+import pytest
+import torch
+
+import nvfp4_w4a4_quantized_08_b200 as nv
+from nvfp4_w4a4_quantized_08_b200 import _native as N
+from nvfp4_w4a4_quantized_08_b200 import build as nbuild
+
+FAKE = 0x7F0000001000  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    nbuild.build()
+    return N.lib()
+
+
+def _weights(rows=1000, cols=4096, layout=N.SF_MMA128x4):
+    return N.Tensor(FAKE, FAKE, FAKE, rows, cols, layout)
+
+
+def _gemv(L, **kw):
+    a = dict(x=FAKE, xd=N.BF16, m=1, ldx=4096, w=_weights(), y=FAKE, yd=N.BF16, ldy=1000,
+             act=N.ACT_NONE)
+    a.update(kw)
+    return L.nvfp4_gemv(a["x"], a["xd"], a["m"], a["ldx"], ctypes.byref(a["w"]), a["y"], a["yd"],
+                        a["ldy"], a["act"], None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(x=None), N.ERR_INVALID_ARG), (dict(y=None), N.ERR_INVALID_ARG),
+    (dict(xd=2), N.ERR_INVALID_ARG), (dict(yd=-1), N.ERR_INVALID_ARG),
+    (dict(act=2), N.ERR_INVALID_ARG), (dict(m=0), N.ERR_INVALID_ARG),
+    (dict(m=-1), N.ERR_INVALID_ARG), (dict(ldx=4095), N.ERR_INVALID_ARG),
+    (dict(ldy=999), N.ERR_INVALID_ARG), (dict(m=17), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(w=_weights(cols=4080)), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(w=_weights(layout=7)), N.ERR_INVALID_ARG),
+    (dict(w=_weights(rows=0)), N.ERR_INVALID_ARG),
+    (dict(x=FAKE + 8), N.ERR_MISALIGNED), (dict(ldx=4100), N.ERR_MISALIGNED),
+    (dict(xd=N.FP32, ldx=4098), N.ERR_MISALIGNED), (dict(y=FAKE + 1), N.ERR_MISALIGNED),
+    (dict(y=FAKE + 2, yd=N.FP32), N.ERR_MISALIGNED)])
+def test_gemv_rejects(L, bad, status):
+    assert _gemv(L, **bad) == status
+
+
+PLAN = dict(cached=FAKE, new=FAKE + 0x1000, batch=4, table=FAKE + 0x2000, stride=8, pages=8,
+            free=FAKE + 0x3000, n_free=10, head=FAKE + 0x4000, page=16, n_pages=100,
+            seq=FAKE + 0x5000, cu=FAKE + 0x6000, slots=FAKE + 0x7000, max_new=20,
+            head_out=FAKE + 0x8000, ws=FAKE + 0x9000, ws_bytes=256)
+
+
+def _plan(L, **kw):
+    a = dict(PLAN, **kw)
+    return L.nvfp4_plan_pages(a["cached"], a["new"], a["batch"], a["table"], a["stride"],
+                              a["pages"], a["free"], a["n_free"], a["head"], a["page"],
+                              a["n_pages"], a["seq"], a["cu"], a["slots"], a["max_new"],
+                              a["head_out"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(batch=-1), N.ERR_INVALID_ARG), (dict(pages=9), N.ERR_INVALID_ARG),
+    (dict(cached=None), N.ERR_INVALID_ARG), (dict(new=None), N.ERR_INVALID_ARG),
+    (dict(table=None), N.ERR_INVALID_ARG), (dict(free=None), N.ERR_INVALID_ARG),
+    (dict(head=None), N.ERR_INVALID_ARG), (dict(seq=None), N.ERR_INVALID_ARG),
+    (dict(cu=None), N.ERR_INVALID_ARG), (dict(slots=None), N.ERR_INVALID_ARG),
+    (dict(head_out=None), N.ERR_INVALID_ARG), (dict(max_new=-1), N.ERR_INVALID_ARG),
+    (dict(n_free=-1), N.ERR_INVALID_ARG), (dict(n_pages=0), N.ERR_INVALID_ARG),
+    (dict(page=0), N.ERR_INVALID_ARG), (dict(page=24), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(page=8192), N.ERR_UNSUPPORTED_SHAPE), (dict(n_pages=1 << 27), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(batch=8193), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(pages=1 << 27, stride=1 << 27), N.ERR_UNSUPPORTED_SHAPE),
+    # outputs that are inputs, or one another, in whole or in part
+    (dict(head_out=FAKE + 0x4000), N.ERR_INVALID_ARG), (dict(seq=FAKE), N.ERR_INVALID_ARG),
+    (dict(seq=FAKE + 0x1000), N.ERR_INVALID_ARG), (dict(cu=FAKE + 0x5000 + 12), N.ERR_INVALID_ARG),
+    (dict(slots=FAKE + 0x2000 + 4 * 31), N.ERR_INVALID_ARG),
+    (dict(slots=FAKE + 2), N.ERR_MISALIGNED),
+    (dict(ws=None), N.ERR_WORKSPACE), (dict(ws_bytes=16), N.ERR_WORKSPACE),
+    (dict(ws=FAKE + 8), N.ERR_MISALIGNED)])
+def test_plan_rejects(L, bad, status):
+    assert _plan(L, **bad) == status
+
+
+def _cache8(**kw):
+    a = dict(k=FAKE, v=FAKE, ks=FAKE, vs=FAKE, n_pages=100, page=16, heads=8, dim=128)
+    a.update(kw)
+    return N.Kv8Cache(a["k"], a["v"], a["ks"], a["vs"], a["n_pages"], a["page"], a["heads"],
+                      a["dim"])
+
+
+BAD_CACHES = [
+    (dict(k=None), N.ERR_INVALID_ARG), (dict(vs=None), N.ERR_INVALID_ARG),
+    (dict(n_pages=0), N.ERR_INVALID_ARG), (dict(heads=0), N.ERR_INVALID_ARG),
+    (dict(page=-16), N.ERR_INVALID_ARG), (dict(page=20), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(page=4112), N.ERR_UNSUPPORTED_SHAPE), (dict(dim=96), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(dim=256), N.ERR_UNSUPPORTED_SHAPE), (dict(heads=65536), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(n_pages=1 << 27), N.ERR_UNSUPPORTED_SHAPE), (dict(k=FAKE + 8), N.ERR_MISALIGNED),
+    (dict(ks=FAKE + 2), N.ERR_MISALIGNED)]
+
+
+def _append(L, cache, **kw):
+    a = dict(k=FAKE, v=FAKE, stride=1024, tokens=5, slots=FAKE, ws=FAKE, ws_bytes=256)
+    a.update(kw)
+    return L.nvfp4_kv8_append(ctypes.byref(cache), a["k"], a["v"], a["stride"], a["tokens"],
+                              a["slots"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_append_rejects_caches(L, bad, status):
+    assert _append(L, _cache8(**bad)) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(k=None), N.ERR_INVALID_ARG), (dict(v=None), N.ERR_INVALID_ARG),
+    (dict(slots=None), N.ERR_INVALID_ARG), (dict(tokens=-1), N.ERR_INVALID_ARG),
+    (dict(tokens=1 << 30), N.ERR_UNSUPPORTED_SHAPE), (dict(stride=1016), N.ERR_INVALID_ARG),
+    (dict(stride=1028), N.ERR_MISALIGNED), (dict(k=FAKE + 8), N.ERR_MISALIGNED),
+    (dict(slots=FAKE + 1), N.ERR_MISALIGNED), (dict(ws=None), N.ERR_WORKSPACE),
+    (dict(ws_bytes=255), N.ERR_WORKSPACE)])
+def test_append_rejects(L, bad, status):
+    assert _append(L, _cache8(), **bad) == status
+
+
+def _attention(L, cache, **kw):
+    a = dict(cu=FAKE, lens=FAKE, table=FAKE, stride=10, batch=2, pages=10, max_q=3, max_kv=160,
+             q=FAKE, qs=4096, tq=6, heads=32, causal=1, scale=0.1, out=FAKE, os=4096, lse=None,
+             scratch=FAKE, sb=1 << 40, ws=FAKE, wb=256)
+    a.update(kw)
+    b = N.Kv8Batch(a["cu"], a["lens"], a["table"], a["stride"], a["batch"], a["pages"],
+                   a["max_q"], a["max_kv"])
+    return L.nvfp4_kv8_attention(ctypes.byref(cache), ctypes.byref(b), a["q"], a["qs"], a["tq"],
+                                 a["heads"], a["causal"], a["scale"], a["out"], a["os"], a["lse"],
+                                 a["scratch"], a["sb"], a["ws"], a["wb"], None)
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_attention_rejects_caches(L, bad, status):
+    assert _attention(L, _cache8(**bad)) == status
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(cu=None), N.ERR_INVALID_ARG), (dict(lens=None), N.ERR_INVALID_ARG),
+    (dict(table=None), N.ERR_INVALID_ARG), (dict(q=None), N.ERR_INVALID_ARG),
+    (dict(out=None), N.ERR_INVALID_ARG), (dict(batch=0), N.ERR_INVALID_ARG),
+    (dict(pages=0), N.ERR_INVALID_ARG), (dict(stride=9), N.ERR_INVALID_ARG),
+    (dict(max_q=0), N.ERR_INVALID_ARG), (dict(max_kv=0), N.ERR_INVALID_ARG),
+    (dict(tq=-1), N.ERR_INVALID_ARG), (dict(heads=0), N.ERR_INVALID_ARG),
+    (dict(heads=12), N.ERR_INVALID_ARG), (dict(causal=2), N.ERR_INVALID_ARG),
+    (dict(scale=0.0), N.ERR_INVALID_ARG), (dict(scale=float("nan")), N.ERR_INVALID_ARG),
+    (dict(scale=float("inf")), N.ERR_INVALID_ARG), (dict(qs=4088), N.ERR_INVALID_ARG),
+    (dict(os=4088), N.ERR_INVALID_ARG), (dict(batch=65536), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(tq=1 << 27), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(pages=1 << 27, stride=1 << 27), N.ERR_UNSUPPORTED_SHAPE),
+    (dict(qs=4100), N.ERR_MISALIGNED), (dict(os=4100), N.ERR_MISALIGNED),
+    (dict(q=FAKE + 8), N.ERR_MISALIGNED), (dict(out=FAKE + 8), N.ERR_MISALIGNED),
+    (dict(lse=FAKE + 2), N.ERR_MISALIGNED), (dict(scratch=FAKE + 8), N.ERR_MISALIGNED),
+    (dict(ws=None), N.ERR_WORKSPACE), (dict(wb=16), N.ERR_WORKSPACE)])
+def test_attention_rejects(L, bad, status):
+    assert _attention(L, _cache8(), **bad) == status
+
+
+def test_status_string(L):
+    assert N.status_string(N.ERR_CAPACITY) == "page pool, block table or slot map too small"
+
+
+def _cpu_cache():
+    return nv.KVCache8.empty(4, 16, 2, 64, device="cpu")
+
+
+def test_binding_refuses_before_the_library():
+    c = _cpu_cache()
+    good = dict(q=torch.zeros(3, 4, 64, dtype=torch.bfloat16),
+                cu_q=torch.zeros(3, dtype=torch.int32), seq_lens=torch.zeros(2, dtype=torch.int32),
+                block_table=torch.zeros(2, 2, dtype=torch.int32))
+    for name, t in [
+            ("q", torch.zeros(3, 4, 64)), ("q", torch.zeros(3, 256, dtype=torch.bfloat16)),
+            ("q", torch.zeros(3, 4, 128, dtype=torch.bfloat16)[..., ::2]),
+            ("q", torch.zeros(4, 3, 64, dtype=torch.bfloat16).transpose(0, 1)),
+            ("cu_q", torch.zeros(2, dtype=torch.int32)), ("cu_q", torch.zeros(3)),
+            ("cu_q", torch.zeros(6, dtype=torch.int32)[::2]),
+            ("seq_lens", torch.zeros(2, dtype=torch.int64)),
+            ("block_table", torch.zeros(3, 2, dtype=torch.int32)),
+            ("block_table", torch.zeros(2, 2, dtype=torch.int32).t().contiguous().t())]:
+        with pytest.raises(ValueError):
+            c.attention(**{**good, name: t})
+    with pytest.raises(ValueError):
+        c.attention(**good, out=torch.zeros(2, 4, 64, dtype=torch.bfloat16))
+    kv = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    slots = torch.zeros(3, dtype=torch.int32)
+    for k, v, s in [(kv.float(), kv, slots), (kv, kv[:2], slots), (kv, kv, slots[:2]),
+                    (kv, kv, slots.long()), (kv[:, :1], kv[:, :1], slots),
+                    (kv, torch.zeros(3, 4, 64, dtype=torch.bfloat16)[:, :2], slots)]:
+        with pytest.raises(ValueError):
+            c.append(k, v, s)
+    for bad in (lambda: nv.KVCache8(c.k_codes.view(torch.uint8), c.v_codes, c.k_scale, c.v_scale),
+                lambda: nv.KVCache8(c.k_codes, c.v_codes[:2], c.k_scale, c.v_scale),
+                lambda: nv.KVCache8(c.k_codes, c.v_codes, c.k_scale.double(), c.v_scale),
+                lambda: nv.KVCache8(c.k_codes, c.v_codes, c.k_scale[:2], c.v_scale),
+                lambda: nv.KVCache8(c.k_codes.transpose(1, 2), c.v_codes.transpose(1, 2),
+                                    c.k_scale, c.v_scale)):
+        with pytest.raises(ValueError):
+            bad()
+    i = torch.zeros(2, dtype=torch.int32)
+    for args in [(i.long(), i, i.view(2, 1), i, i[:1]), (i, i[:1], i.view(2, 1), i, i[:1]),
+                 (i, i, i, i, i[:1]), (i, i, i.view(2, 1), i, i),
+                 (i, i, torch.zeros(4, 2, dtype=torch.int32), i, i[:1])]:
+        with pytest.raises(ValueError):
+            nv.plan_pages(*args, page_tokens=16, n_pages=4, max_new=3)
+    w = nv.NVFP4Tensor(torch.zeros(8, 16, dtype=torch.uint8), torch.zeros(512, dtype=torch.uint8),
+                       torch.zeros(1), 8, 32, nv.SF_MMA128x4)
+    x = torch.zeros(2, 32)
+    for bad in (dict(x=x[0]), dict(x=x[:, :16]), dict(x=x.t().contiguous().t()),
+                dict(x=x, out=torch.zeros(1, 8)), dict(x=x, out=torch.zeros(2, 7))):
+        with pytest.raises(ValueError):
+            nv.gemv(w=w, **bad)
+    for bad in (dict(x=x.half()), dict(x=x, out=torch.zeros(2, 8).half())):
+        with pytest.raises(TypeError):
+            nv.gemv(w=w, **bad)
