@@ -31,11 +31,13 @@ def workspace(device=None) -> torch.Tensor:
     """A zero-filled workspace for the current stream of `device` (cached).
     Calls that share it must stay ordered on that stream."""
     idx = None if device is None else torch.device(device).index
-    dev = torch.device("cuda", torch.cuda.current_device() if idx is None else idx)
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    if idx is None:
+        idx = torch.cuda.current_device()
+    key = (idx, torch._C._cuda_getCurrentRawStream(idx))
     ws = _workspaces.get(key)
     if ws is None:
-        ws = torch.zeros(N.lib().nvfp4_workspace_bytes(), dtype=torch.uint8, device=dev)
+        ws = torch.zeros(N.lib().nvfp4_workspace_bytes(), dtype=torch.uint8,
+                         device=torch.device("cuda", idx))
         _workspaces[key] = ws
     return ws
 
@@ -238,21 +240,24 @@ def _launch(fn, what: str, device: torch.device, *args) -> None:
     """Calls an entry point on `device`'s current stream, with `device` current."""
     if device.type != "cuda":
         raise ValueError(f"{what} takes CUDA tensors")
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    i = device.index
+    if i == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    if status != N.OK:
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if status:
         raise NVFP4Error(status, what)
 
 
-def _check_int32(device: torch.device, **tensors: torch.Tensor) -> None:
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or t.device != device:
-            raise ValueError(f"{name} must be an int32 tensor on {device}")
-        if t.dim() != 2 and (t.dim() != 1 or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous, of one dimension")
+def _check_int32(device: torch.device, name: str, t: torch.Tensor, dims: int = 1) -> None:
+    if t.dtype is not torch.int32 or t.device != device or t.dim() != dims:
+        raise ValueError(f"{name} must be an int32 tensor of {dims} dimension(s) on {device}")
+    if dims == 1:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    elif t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
 
 
 def _row_stride(t: torch.Tensor) -> int:
@@ -270,7 +275,7 @@ def gemv(x: torch.Tensor, w: NVFP4Tensor, out_dtype: torch.dtype = torch.bfloat1
     if x.device != w.device:
         raise ValueError("x and w must be on one device")
     if out is None:
-        out = torch.empty(x.shape[0], w.rows, dtype=out_dtype, device=x.device)
+        out = torch.empty((x.shape[0], w.rows), dtype=out_dtype, device=x.device)
     elif (out.dim() != 2 or out.shape[0] != x.shape[0] or out.shape[1] < w.rows or
           out.stride(1) != 1 or out.device != x.device):
         raise ValueError(f"out must have {x.shape[0]} rows of at least {w.rows} unit-stride "
@@ -299,21 +304,27 @@ def plan_pages(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     new tensors (free_head of the result goes into the next call).  Lengths that
     do not fit are reported by device_status, and then change nothing."""
     dev = block_table.device
-    _check_int32(dev, cached_lens=cached_lens, new_lens=new_lens, block_table=block_table,
-                 free_pages=free_pages, free_head=free_head)
-    batch = cached_lens.shape[0]
-    if (block_table.dim() != 2 or block_table.shape[0] != batch or new_lens.shape[0] != batch or
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1) or free_head.numel() != 1):
-        raise ValueError("plan_pages: block_table must be [batch, max_pages] with unit column "
-                         "stride, new_lens [batch], free_head [1]")
-    seq, cu = cached_lens.new_empty(batch), cached_lens.new_empty(batch + 1)
-    slots, head = cached_lens.new_empty(max_new), cached_lens.new_empty(1)
+    _check_int32(dev, "cached_lens", cached_lens)
+    _check_int32(dev, "new_lens", new_lens)
+    _check_int32(dev, "block_table", block_table, 2)
+    _check_int32(dev, "free_pages", free_pages)
+    _check_int32(dev, "free_head", free_head)
+    batch, max_pages = block_table.shape
+    if cached_lens.shape[0] != batch or new_lens.shape[0] != batch or free_head.shape[0] != 1:
+        raise ValueError("plan_pages: cached_lens and new_lens must be [batch], block_table "
+                         "[batch, max_pages], free_head [1]")
+    if max_new < 0:
+        raise ValueError("max_new must not be negative")
+    # one allocation for the four results, each on a 16-byte boundary
+    a, b = (batch + 3) // 4 * 4, (batch + 4) // 4 * 4
+    mem = torch.empty(4 + a + b + max_new, dtype=torch.int32, device=dev)
+    head, seq, cu, slots = mem[:1], mem[4:4 + batch], mem[4 + a:5 + a + batch], mem[4 + a + b:]
     ws = workspace(dev) if ws is None else ws
+    at = mem.data_ptr()
     _launch(N.lib().nvfp4_plan_pages, "nvfp4_plan_pages", dev, cached_lens.data_ptr(),
-            new_lens.data_ptr(), batch, block_table.data_ptr(),
-            _row_stride(block_table), block_table.shape[1],
-            free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(), page_tokens, n_pages,
-            seq.data_ptr(), cu.data_ptr(), slots.data_ptr(), max_new, head.data_ptr(),
+            new_lens.data_ptr(), batch, block_table.data_ptr(), _row_stride(block_table),
+            max_pages, free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(),
+            page_tokens, n_pages, at + 16, at + 16 + 4 * a, at + 16 + 4 * (a + b), max_new, at,
             ws.data_ptr(), ws.numel())
     return PagePlan(seq, cu, slots, head)
 
@@ -359,14 +370,17 @@ class KVCache8:
         heads * head_dim] whose tokens are contiguous."""
         d = self.head_dim
         if t.dim() == 3:
-            ok = t.shape[1] == heads and t.shape[2] == d and t.stride(2) == 1 and \
-                (heads == 1 or t.stride(1) == d)
+            n, h, e = t.shape
+            stride, sh, se = t.stride()
+            ok = h == heads and e == d and se == 1 and (sh == d or heads == 1)
         else:
-            ok = t.dim() == 2 and t.shape[1] == heads * d and t.stride(1) == 1
-        if not ok or t.dtype != torch.bfloat16 or t.device != self.k_codes.device:
+            n, e = t.shape if t.dim() == 2 else (0, -1)
+            stride = t.stride(0) if t.dim() == 2 else 0
+            ok = e == heads * d and t.stride(1) == 1
+        if not ok or t.dtype is not torch.bfloat16 or t.device != self.k_codes.device:
             raise ValueError(f"{name} must be a bf16 tensor [tokens, {heads}, {d}] on "
                              f"{self.k_codes.device}, contiguous inside a token")
-        return t.stride(0) if t.shape[0] > 1 else heads * d
+        return stride if n > 1 else heads * d
 
     def append(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
                ws: Optional[torch.Tensor] = None) -> None:
@@ -377,8 +391,8 @@ class KVCache8:
         tokens = k.shape[0]
         if v.shape[0] != tokens or self._rows("v", v, self.kv_heads) != stride:
             raise ValueError("k and v must share their tokens and a token stride")
-        _check_int32(k.device, slot_map=slot_map)
-        if slot_map.dim() != 1 or slot_map.shape[0] < tokens:
+        _check_int32(k.device, "slot_map", slot_map)
+        if slot_map.shape[0] < tokens:
             raise ValueError(f"slot_map must have at least {tokens} entries")
         ws = workspace(k.device) if ws is None else ws
         cs = self.c_struct()
@@ -410,20 +424,21 @@ class KVCache8:
         tokens, heads = q.shape[0], q.shape[1]
         stride = self._rows("q", q, heads)
         dev = q.device
-        _check_int32(dev, cu_q=cu_q, seq_lens=seq_lens, block_table=block_table)
-        batch = seq_lens.shape[0]
-        if (cu_q.dim() != 1 or seq_lens.dim() != 1 or cu_q.shape[0] != batch + 1 or
-                block_table.dim() != 2 or block_table.shape[0] != batch or
-                (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        _check_int32(dev, "cu_q", cu_q)
+        _check_int32(dev, "seq_lens", seq_lens)
+        _check_int32(dev, "block_table", block_table, 2)
+        batch, pages = block_table.shape
+        if cu_q.shape[0] != batch + 1 or seq_lens.shape[0] != batch:
             raise ValueError("attention: cu_q must be [batch + 1], seq_lens [batch] and "
-                             "block_table [batch, pages] with unit column stride")
+                             "block_table [batch, pages]")
         if out is None:
-            out = torch.empty(tokens, heads, self.head_dim, dtype=torch.bfloat16, device=dev)
+            out = torch.empty((tokens, heads, self.head_dim), dtype=torch.bfloat16, device=dev)
+            out_stride = heads * self.head_dim
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
-        out_stride = self._rows("out", out, heads)
-        lse = torch.empty(tokens, heads, dtype=torch.float32, device=dev) if return_lse else None
-        pages = block_table.shape[1]
+        else:
+            out_stride = self._rows("out", out, heads)
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
         cs = self.c_struct()
         cb = N.Kv8Batch(cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
                         _row_stride(block_table), batch, pages,
