@@ -6,14 +6,17 @@
 // Bound by the cache: each K and V byte is read once for the rows of one request
 // that share a KV head (G query heads times the request's queries, packed; tiles of
 // 8 NT rows).  One CTA takes one tile of rows, one KV head and one range of tokens;
-// its four warps take groups of 16 tokens in turn, straight from global memory into
-// registers (2 KB of K and 2 KB of V a group and warp for 128 dims, the next group's
-// loads issued before the current one is computed), with no shared memory on the way:
+// its four warps take groups of 16 tokens in turn (2 KB of K and 2 KB of V for 128
+// dims), each through a ring of its own in shared memory that asynchronous 16-byte
+// copies fill kStages - 1 groups ahead: ~144 KB in flight an SM, where the latency of
+// HBM at full rate needs ~40 KB and two groups a warp in registers gave 48 KB in
+// theory and 62% of the rate.  Rings are private to a warp, so no barrier is waited on.
 //
 //   S^T = K Q^T    m16n8k16, A = 16 tokens of K, B = 8 rows of Q.  The order of the
 //                  dims inside a product is free, so a lane's 32 contiguous bytes of a
 //                  token are its A registers after one hardware conversion (E4M3 ->
-//                  fp16, exact) per two elements.
+//                  fp16, exact) per two elements (a table or shifts cost 2.5 times the
+//                  issue slots: 10 against 25 words a clock and SM, measured).
 //   O^T += V^T P^T m16n8k16, A = 16 dims by 16 tokens of V: a lane loads 16 contiguous
 //                  dims of its four tokens and pairs tokens with byte permutes before
 //                  the conversion.  P^T comes from S^T by an 8x8 transposition in
@@ -32,6 +35,8 @@
 // Ranges: with few requests and heads the tokens are split over CTAs; each leaves its
 // normalised rows in fp32 and their log-sum-exp, and a second kernel joins them in
 // order of the range, so results do not depend on timing.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv8_batch.cuh"
@@ -41,6 +46,7 @@ namespace kv8 {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 4;
 constexpr float kLazy = 8.0f;
 constexpr float kBias = 7.0f;   // weights are taken times 2^7: at most 2^15 in fp16
 constexpr float kNegInf = -INFINITY;
@@ -77,39 +83,45 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return y;
 }
 
-// Code words of one lane for one group of 16 tokens, and the group's page scales.
-template <int kDim>
-struct Group {
-  static constexpr int kWords = kDim / 16;  // words of one token's share: K dims / 4 lanes
-  uint32_t k[2][kWords];                    // tokens r and r + 8, dims [dim / 4 * c, ..)
-  uint32_t v[4][kDim / 32];                 // tokens 2c, 2c+1, 2c+8, 2c+9, dims [dim / 8 * r, ..)
-  float ks, vs;
-};
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 template <int kWords>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[kWords]) {
-  if constexpr (kWords == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = v.x;
-    w[1] = v.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kWords / 4; ++i) {
-      const uint4 v = ld_nc_v4(p + 16 * i);
-      w[4 * i] = v.x;
-      w[4 * i + 1] = v.y;
-      w[4 * i + 2] = v.z;
-      w[4 * i + 3] = v.w;
-    }
-  }
+__device__ __forceinline__ void lds(uint32_t at, uint32_t* w) {
+  if constexpr (kWords == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(at));
+  else
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+}
+
+// Where byte `at` of a 16-token group's codes lies in its stage: 16-byte units of a token
+// row exchanged by the token's place, so that the reads below meet no bank twice (128 dims)
+// or at most twice (64).
+template <int kDim>
+__device__ __forceinline__ uint32_t place(uint32_t token, uint32_t unit) {
+  if constexpr (kDim == 128)
+    return token * 128 + ((unit ^ (token & 7)) << 4);
+  else
+    return token * 64 + ((unit ^ ((token >> 1) & 3)) << 4);
 }
 
 template <int kDim, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
   constexpr int kSteps = kDim / 16;   // k16 steps of S
   constexpr int kTiles = kDim / 16;   // m16 tiles of O
   constexpr int kRows = 8 * NT;
-  __shared__ float so[kWarps][kRows][kDim + 4];
+  constexpr int kGroup = 16 * kDim;   // bytes of K (and of V) of a group
+  extern __shared__ __align__(128) uint8_t ring[];   // [warp][stage][K, V][kGroup]
+  // after the last group: the warps' rows, in the rings' place
+  float (*so)[kRows][kDim + 4] = reinterpret_cast<float (*)[kRows][kDim + 4]>(ring);
   __shared__ float sm[kWarps][3][kRows];   // maximum, weights' maximum, sum
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
   const int split = blockIdx.x % a.n_splits, tile = blockIdx.x / a.n_splits;
@@ -183,46 +195,86 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_kernel(const
     for (int i = 0; i < 2; ++i) l[nt][i] = 0.0f, m[nt][i] = kNegInf, mv[nt][i] = kNegInf;
   }
 
-  // page of every group of this warp, 32 groups at a time: lane i holds group i's
+  // this warp's groups: tokens first + 64 i .. + 15
+  const int first = t_begin + 16 * warp;
+  const int n_groups = t_end > first ? (t_end - first + 16 * kWarps - 1) / (16 * kWarps) : 0;
+  // page and page scales of 32 groups at a time, lane j's those of group j; two windows,
+  // the second loaded while the first is worked on
   const int32_t* table = a.table + int64_t(b) * a.table_stride;
-  int pages = 0;
-  auto load_pages = [&](int g0) {
-    const int tok = t_begin + (g0 + lane) * (16 * kWarps) + 16 * warp;
-    pages = tok < t_end ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : 0;
+  struct Window {
+    int page;
+    float ks, lv;   // lv: log2 of the V scale
   };
-  auto load = [&](int gi, Group<kDim>& g) {
-    const int tok = t_begin + gi * (16 * kWarps) + 16 * warp;
-    const int id = __shfl_sync(0xFFFFFFFFu, pages, gi & 31);
-    if (tok >= t_end) return;
+  auto load_pages = [&](int i0) {
+    const int tok = first + (i0 + lane) * (16 * kWarps);
+    return i0 + lane < n_groups ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : 0;
+  };
+  auto load_scales = [&](int i0, int id) {
+    Window w;
     const bool ok = id >= 0 && id < a.n_pages;
-    const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
-    const int64_t ph = int64_t(ok ? id : 0) * a.kv_heads + h;
-    const int64_t at = (ph * a.page_tokens + in_page) * kDim;
-    const uint8_t* kp = a.k_codes + at + r * kDim + c * (kDim / 4);
-    load_words(kp, g.k[0]);
-    load_words(kp + 8 * kDim, g.k[1]);
-    const uint8_t* vp = a.v_codes + at + 2 * c * kDim + r * (kDim / 8);
-    load_words(vp, g.v[0]);
-    load_words(vp + kDim, g.v[1]);
-    load_words(vp + 8 * kDim, g.v[2]);
-    load_words(vp + 9 * kDim, g.v[3]);
+    w.page = ok ? id : 0;
+    const int64_t ph = int64_t(w.page) * a.kv_heads + h;
     // a page that is not one of the pool's is left out, and recorded
-    g.ks = ok ? __ldg(a.k_scale + ph) : kNegInf;
-    g.vs = __ldg(a.v_scale + ph);
-    if (!ok && lane == 0) record_status(a.status, NVFP4_ERR_INVALID_ARG);
+    if (!ok && i0 + lane < n_groups) record_status(a.status, NVFP4_ERR_INVALID_ARG);
+    w.ks = ok ? __ldg(a.k_scale + ph) : kNegInf;
+    // log2 of the V scale, exact for a power of two; -inf for 0 (a page never written)
+    const uint32_t vb = __float_as_uint(__ldg(a.v_scale + ph));
+    w.lv = vb < 0x00800000u ? kNegInf
+                            : float(int(vb >> 23) - 127) +
+                                  __log2f(__uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u));
+    return w;
+  };
+  const uint32_t my_ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
+                           uint32_t(warp) * kStages * 2 * kGroup;
+  // copies group i into its stage (nothing past the last; the group is committed all the same)
+  auto issue = [&](int i, const Window& w) {
+    const int page = __shfl_sync(0xFFFFFFFFu, w.page, i & 31);
+    if (i < n_groups) {
+      const int tok = first + i * (16 * kWarps);
+      const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
+      const int64_t at =
+          ((int64_t(page) * a.kv_heads + h) * a.page_tokens + in_page) * kDim + lane * 16;
+      const uint32_t dst = my_ring + uint32_t(i % kStages) * 2 * kGroup;
+#pragma unroll
+      for (int j = 0; j < kGroup / 512; ++j) {
+        const uint32_t n = lane + 32 * j;
+        const uint32_t d = place<kDim>(n / (kDim / 16), n % (kDim / 16));
+        copy16(dst + d, a.k_codes + at + 512 * j);
+        copy16(dst + kGroup + d, a.v_codes + at + 512 * j);
+      }
+    }
+    copies_commit();
   };
 
-  auto compute = [&](int gi, Group<kDim>& g) {
-    const int tok = t_begin + gi * (16 * kWarps) + 16 * warp;
-    const bool bad = g.ks == kNegInf;
+  auto compute = [&](int i, const Window& win) {
+    const int tok = first + i * (16 * kWarps);
+    const float ks_page = __shfl_sync(0xFFFFFFFFu, win.ks, i & 31);
+    const float lv = __shfl_sync(0xFFFFFFFFu, win.lv, i & 31);
+    const bool bad = ks_page == kNegInf;
+    const uint32_t kst = my_ring + uint32_t(i % kStages) * 2 * kGroup, vst = kst + kGroup;
+    // K: tokens r and r + 8, dims [kDim / 4 * c, ..); V: tokens 2c, 2c + 1, 2c + 8, 2c + 9,
+    // dims [kDim / 8 * r, ..)
+    uint32_t kk[2][kDim / 16], vv[4][kDim / 32];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < kDim / 64; ++j)
+        lds<4>(kst + place<kDim>(r + 8 * t, c * (kDim / 64) + j), &kk[t][4 * j]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int token = 2 * c + (t & 1) + 8 * (t >> 1);
+      if constexpr (kDim == 128)
+        lds<4>(vst + place<kDim>(token, r), vv[t]);
+      else
+        lds<2>(vst + place<kDim>(token, r >> 1) + 8 * (r & 1), vv[t]);
+    }
     // V of tokens past the request's end may be anything, NaN codes included: zero
     if (bad || tok + 16 > rq.kv) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = tok + 2 * c + (i & 1) + 8 * (i >> 1);
-        if (bad || t >= rq.kv) {
+      for (int t = 0; t < 4; ++t) {
+        if (bad || tok + 2 * c + (t & 1) + 8 * (t >> 1) >= rq.kv) {
 #pragma unroll
-          for (int j = 0; j < kDim / 32; ++j) g.v[i][j] = 0;
+          for (int j = 0; j < kDim / 32; ++j) vv[t][j] = 0;
         }
       }
     }
@@ -230,27 +282,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_kernel(const
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+      for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) {
       uint32_t a0, a1, a2, a3;
-      e4m3_f16(g.k[0][ks], a0, a2);
-      e4m3_f16(g.k[1][ks], a1, a3);
+      e4m3_f16(kk[0][ks], a0, a2);
+      e4m3_f16(kk[1][ks], a1, a3);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
     }
-    // log2 of the V scale, exact for a power of two; -inf for 0 (a page never written)
-    const uint32_t vb = __float_as_uint(g.vs);
-    const float lv = vb < 0x00800000u ? kNegInf
-                                      : float(int(vb >> 23) - 127) +
-                                            __log2f(__uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u));
     const bool masked = bad || tok + 16 > t_range || tok + 16 > vis_all;
     bool raise = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float f = qs[nt][i] * g.ks;
+        const float f = qs[nt][i] * ks_page;
         s[nt][i] *= f;
         s[nt][2 + i] *= f;
         if (masked) {
@@ -301,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_kernel(const
 #pragma unroll
     for (int j = 0; j < kDim / 32; ++j) {
       // words j of four tokens: dims 4 j .. 4 j + 3 of the lane's, two O tiles
-      const uint32_t x0 = prmt(g.v[0][j], g.v[1][j], 0x5140), x1 = prmt(g.v[0][j], g.v[1][j], 0x7362);
-      const uint32_t y0 = prmt(g.v[2][j], g.v[3][j], 0x5140), y1 = prmt(g.v[2][j], g.v[3][j], 0x7362);
+      const uint32_t x0 = prmt(vv[0][j], vv[1][j], 0x5140), x1 = prmt(vv[0][j], vv[1][j], 0x7362);
+      const uint32_t y0 = prmt(vv[2][j], vv[3][j], 0x5140), y1 = prmt(vv[2][j], vv[3][j], 0x7362);
       uint32_t a0, a1, a2, a3;
       e4m3_f16(x0, a0, a1);
       e4m3_f16(y0, a2, a3);
@@ -316,21 +363,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) decode_kernel(const
     }
   };
 
-  const int n_groups = (max(t_end - t_begin, 0) + 16 * kWarps - 1) / (16 * kWarps);
-  Group<kDim> ga, gb;
-  if (n_groups > 0) {
-    load_pages(0);
-    load(0, ga);
-  }
-  for (int gi = 0; gi < n_groups; gi += 2) {
-    if (gi + 1 < n_groups) load(gi + 1, gb);
-    if (t_begin + gi * (16 * kWarps) + 16 * warp < t_end) compute(gi, ga);
-    if (gi + 1 < n_groups) {
-      if (((gi + 2) & 31) == 0) load_pages(gi + 2);
-      if (gi + 2 < n_groups) load(gi + 2, ga);
-      if (t_begin + (gi + 1) * (16 * kWarps) + 16 * warp < t_end) compute(gi + 1, gb);
+  Window cur = load_scales(0, load_pages(0)), nxt = cur;
+  int next_page = load_pages(32);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i, cur);
+  for (int i = 0; i < n_groups; ++i) {
+    // the window of the groups that are copied runs kStages - 1 ahead of the computed ones'
+    if ((i & 31) == 16) nxt = load_scales((i & ~31) + 32, next_page);
+    if ((i & 31) == 0 && i > 0) {
+      cur = nxt;
+      next_page = load_pages(i + 32);
     }
+    copies_wait<kStages - 2>();
+    __syncwarp();   // group i is there for every lane, and stage i - 1 is read by every lane
+    const int ahead = i + kStages - 1;
+    issue(ahead, (ahead >> 5) == (i >> 5) ? cur : nxt);
+    compute(i, cur);
   }
+  copies_wait<0>();
+  __syncthreads();   // the rings are free for the rows
 
   // join the four warps: sums of the lanes' tokens, then maxima and rows through
   // shared memory
@@ -444,10 +495,18 @@ static cudaError_t launch_dim(const Args& a, const Kv8Plan& p, int32_t batch, in
   const dim3 grid(unsigned(p.n_splits) * unsigned(p.row_tiles), unsigned(a.kv_heads),
                   unsigned(batch));
   cudaError_t e = cudaSuccess;
-  if (p.rows == 8)
-    e = launch_pdl(decode_kernel<kDim, 1>, grid, dim3(kThreads), 0, st, a);
-  else
-    e = launch_pdl(decode_kernel<kDim, 2>, grid, dim3(kThreads), 0, st, a);
+  // the rings, or the joined rows if they are larger
+  constexpr size_t kRing = size_t(kWarps) * kStages * 2 * 16 * kDim;
+  constexpr size_t kSmem = std::max(kRing, size_t(kWarps) * 16 * (kDim + 4) * sizeof(float));
+  if (p.rows == 8) {
+    e = allow_smem<decode_kernel<kDim, 1>>(kSmem);
+    if (e == cudaSuccess)
+      e = launch_pdl(decode_kernel<kDim, 1>, grid, dim3(kThreads), kSmem, st, a);
+  } else {
+    e = allow_smem<decode_kernel<kDim, 2>>(kSmem);
+    if (e == cudaSuccess)
+      e = launch_pdl(decode_kernel<kDim, 2>, grid, dim3(kThreads), kSmem, st, a);
+  }
   if (e != cudaSuccess || p.n_splits == 1) return e;
   const int64_t rows = int64_t(max_q) * a.q_heads;
   return launch_pdl(join_kernel<kDim>, dim3(unsigned((rows + kWarps - 1) / kWarps), unsigned(batch)),
