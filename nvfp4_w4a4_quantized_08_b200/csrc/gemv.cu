@@ -352,20 +352,8 @@ cudaError_t launch(const Args& a, int sm_count, cudaStream_t st) {
   // the grid within two CTAs an SM
   int cs = 1;
   while (cs < kMaxCluster && ctas * cs * 2 <= 2 * sm_count && n_steps >= KW * cs * 4) cs *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ctas * cs));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = unsigned(cs);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemv_kernel<KW, NT, FP32>, a);
+  return launch_pdl_cluster(gemv_kernel<KW, NT, FP32>, dim3(unsigned(ctas * cs)),
+                            dim3(unsigned(cs)), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace gemv

@@ -168,6 +168,7 @@ struct Kv8Plan {
   int32_t rows;       // rows of a tile
   int32_t row_tiles;  // tiles of a request's rows
   int32_t chunk, n_splits;
+  bool cluster;       // the ranges of a unit are one cluster
   size_t scratch;     // bytes
 };
 Kv8Plan kv8_plan(const LaunchKv8Attn& d);

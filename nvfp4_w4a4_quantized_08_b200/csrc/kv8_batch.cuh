@@ -26,6 +26,7 @@ struct Args {
   FastDiv group_div, page_div;
   float scale_log2;        // softmax scale * log2(e)
   int32_t chunk, n_splits; // tokens of a range, most ranges
+  int32_t cluster;         // the ranges of a unit are a cluster, which joins them itself
   float* part_o;           // [n_splits][tq][q_heads][dim]
   float* part_lse;         // [n_splits][tq][q_heads], base 2
   uint32_t* status;

@@ -37,16 +37,21 @@
 // order of the range, so results do not depend on timing.
 #include <algorithm>
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "kv8_batch.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace nvfp4 {
 namespace kv8 {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
+constexpr int kMaxCluster = 8;
 constexpr float kLazy = 8.0f;
 constexpr float kBias = 7.0f;   // weights are taken times 2^7: at most 2^15 in fp16
 constexpr float kNegInf = -INFINITY;
@@ -113,30 +118,59 @@ __device__ __forceinline__ uint32_t place(uint32_t token, uint32_t unit) {
     return token * 64 + ((unit ^ ((token >> 1) & 3)) << 4);
 }
 
+// Groups of 16 tokens that a warp takes at a time: two of 64 dims, so that the work that
+// goes by tokens, not bytes, has two chains to overlap.
 template <int kDim, int NT>
-__global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
+constexpr int kGroups = kDim == 64 && NT == 1 ? 2 : 1;
+
+// CTAs of an SM: by registers.
+template <int NT>
+constexpr int kResident = NT == 1 ? 4 : 3;
+
+template <int kDim, int NT>
+__global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const Args a) {
   constexpr int kSteps = kDim / 16;   // k16 steps of S
   constexpr int kTiles = kDim / 16;   // m16 tiles of O
   constexpr int kRows = 8 * NT;
   constexpr int kGroup = 16 * kDim;   // bytes of K (and of V) of a group
-  extern __shared__ __align__(128) uint8_t ring[];   // [warp][stage][K, V][kGroup]
+  constexpr int kG = kGroups<kDim, NT>, kStage = kG * 2 * kGroup;
+  constexpr int kStepTokens = 16 * kG * kWarps;
+  extern __shared__ __align__(128) uint8_t ring[];   // [warp][stage][group][K, V][kGroup]
   // after the last group: the warps' rows, in the rings' place
   float (*so)[kRows][kDim + 4] = reinterpret_cast<float (*)[kRows][kDim + 4]>(ring);
   __shared__ float sm[kWarps][3][kRows];   // maximum, weights' maximum, sum
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
-  const int split = blockIdx.x % a.n_splits, tile = blockIdx.x / a.n_splits;
-  const int h = blockIdx.y, b = blockIdx.z;
+  // ranges are the slowest index: the later ones, which fewer requests have, come last
+  const int h = blockIdx.x % a.kv_heads, tile = blockIdx.x / a.kv_heads;
+  const int b = blockIdx.y, split = blockIdx.z;
+  // This warp's steps: kG groups of 16 tokens, tokens first + kStepTokens i ..; a group is
+  // inside one page.  The pages of 32 groups at a time, lane j's that of group j, whether the
+  // request is as long or not: so the first ones are read along with the lengths.
+  const int t_begin = split * a.chunk;
+  const int first = t_begin + 16 * kG * warp;
+  const int32_t* table = a.table + int64_t(b) * a.table_stride;
+  auto group_token = [&](int n) { return first + (n / kG) * kStepTokens + (n % kG) * 16; };
+  auto load_pages = [&](int n0) {
+    const int tok = group_token(n0 + lane);
+    return tok < a.max_tokens ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : 0;
+  };
   pdl_wait();
   pdl_trigger();
-  const Request rq = request(a, b, tid == 0 && blockIdx.x == 0 && h == 0);
+  const int first_page = load_pages(0);
+  int next_page = load_pages(32);
+  const Request rq = request(a, b, tid == 0 && blockIdx.x == 0 && split == 0);
   const int rows = rq.nq * a.group;
   const int rho0 = tile * kRows;
-  if (rho0 >= rows) return;
+  const int used = splits_of(a, rq.kv);
+  if (rho0 >= rows || split >= used) {
+    if (a.cluster) {  // the other CTAs count this one at both barriers
+      cg::this_cluster().sync();
+      cg::this_cluster().sync();
+    }
+    return;
+  }
   // this CTA's tokens: its range, up to what the tile's last row sees
   const int last_row = min(rho0 + kRows, rows) - 1;
-  const int used = splits_of(a, rq.kv);
-  if (split >= used) return;
-  const int t_begin = split * a.chunk;
   const int t_range = split == used - 1 ? rq.kv : min(rq.kv, t_begin + a.chunk);
   const int t_end = min(t_range, sees(a, rq, last_row));
 
@@ -184,7 +218,9 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
   // tokens every row of the tile sees (the first row sees the fewest)
   const int vis_all = sees(a, rq, rho0);
 
-  float o[NT][kTiles][4], l[NT][2], m[NT][2], mv[NT][2];
+  // running maxima: base and basev (less kBias) are what the exponents are taken against, 0
+  // before the first token; lim and limv what a score may reach without a rescale
+  float o[NT][kTiles][4], l[NT][2], base[NT][2], basev[NT][2], lim[NT][2], limv[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -192,30 +228,28 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[nt][t][i] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) l[nt][i] = 0.0f, m[nt][i] = kNegInf, mv[nt][i] = kNegInf;
+    for (int i = 0; i < 2; ++i) {
+      l[nt][i] = base[nt][i] = basev[nt][i] = 0.0f;
+      lim[nt][i] = limv[nt][i] = kNegInf;
+    }
   }
 
-  // this warp's groups: tokens first + 64 i .. + 15
-  const int first = t_begin + 16 * warp;
-  const int n_groups = t_end > first ? (t_end - first + 16 * kWarps - 1) / (16 * kWarps) : 0;
-  // page and page scales of 32 groups at a time, lane j's those of group j; two windows,
-  // the second loaded while the first is worked on
-  const int32_t* table = a.table + int64_t(b) * a.table_stride;
+  const int n_steps = t_end > first ? (t_end - first + kStepTokens - 1) / kStepTokens : 0;
+  // place and page scales of 32 groups at a time; two windows, the second loaded while the
+  // first is worked on
   struct Window {
-    int page;
-    float ks, lv;   // lv: log2 of the V scale
+    int64_t at;     // bytes from the start of the codes
+    float ks, lv;   // scale of K, log2 of the scale of V
   };
-  auto load_pages = [&](int i0) {
-    const int tok = first + (i0 + lane) * (16 * kWarps);
-    return i0 + lane < n_groups ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : 0;
-  };
-  auto load_scales = [&](int i0, int id) {
+  auto load_window = [&](int n0, int id) {
     Window w;
+    const int tok = group_token(n0 + lane);
     const bool ok = id >= 0 && id < a.n_pages;
-    w.page = ok ? id : 0;
-    const int64_t ph = int64_t(w.page) * a.kv_heads + h;
+    const int64_t ph = int64_t(ok ? id : 0) * a.kv_heads + h;
+    const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
+    w.at = (ph * a.page_tokens + in_page) * kDim;
     // a page that is not one of the pool's is left out, and recorded
-    if (!ok && i0 + lane < n_groups) record_status(a.status, NVFP4_ERR_INVALID_ARG);
+    if (!ok && tok < t_end) record_status(a.status, NVFP4_ERR_INVALID_ARG);
     w.ks = ok ? __ldg(a.k_scale + ph) : kNegInf;
     // log2 of the V scale, exact for a power of two; -inf for 0 (a page never written)
     const uint32_t vb = __float_as_uint(__ldg(a.v_scale + ph));
@@ -225,159 +259,208 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
     return w;
   };
   const uint32_t my_ring = static_cast<uint32_t>(__cvta_generic_to_shared(ring)) +
-                           uint32_t(warp) * kStages * 2 * kGroup;
-  // copies group i into its stage (nothing past the last; the group is committed all the same)
-  auto issue = [&](int i, const Window& w) {
-    const int page = __shfl_sync(0xFFFFFFFFu, w.page, i & 31);
-    if (i < n_groups) {
-      const int tok = first + i * (16 * kWarps);
-      const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
-      const int64_t at =
-          ((int64_t(page) * a.kv_heads + h) * a.page_tokens + in_page) * kDim + lane * 16;
-      const uint32_t dst = my_ring + uint32_t(i % kStages) * 2 * kGroup;
+                           uint32_t(warp) * kStages * kStage;
+  uint32_t copy_to[kGroup / 512];   // where this lane's units of a group go
 #pragma unroll
-      for (int j = 0; j < kGroup / 512; ++j) {
-        const uint32_t n = lane + 32 * j;
-        const uint32_t d = place<kDim>(n / (kDim / 16), n % (kDim / 16));
-        copy16(dst + d, a.k_codes + at + 512 * j);
-        copy16(dst + kGroup + d, a.v_codes + at + 512 * j);
+  for (int j = 0; j < kGroup / 512; ++j) {
+    const uint32_t n = lane + 32 * j;
+    copy_to[j] = my_ring + place<kDim>(n / (kDim / 16), n % (kDim / 16));
+  }
+  const uint8_t* k_from = a.k_codes + lane * 16;
+  const uint8_t* v_from = a.v_codes + lane * 16;
+  // copies step i into its stage (nothing past the last; the group is committed all the same)
+  auto issue = [&](int i, const Window& w) {
+    const uint32_t st = uint32_t(i % kStages) * kStage;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      const int64_t at = __shfl_sync(0xFFFFFFFFu, w.at, (i * kG + g) & 31);
+      if (first + i * kStepTokens + 16 * g < t_end) {
+#pragma unroll
+        for (int j = 0; j < kGroup / 512; ++j) {
+          copy16(copy_to[j] + st + g * 2 * kGroup, k_from + at + 512 * j);
+          copy16(copy_to[j] + st + (g * 2 + 1) * kGroup, v_from + at + 512 * j);
+        }
       }
     }
     copies_commit();
   };
 
   auto compute = [&](int i, const Window& win) {
-    const int tok = first + i * (16 * kWarps);
-    const float ks_page = __shfl_sync(0xFFFFFFFFu, win.ks, i & 31);
-    const float lv = __shfl_sync(0xFFFFFFFFu, win.lv, i & 31);
-    const bool bad = ks_page == kNegInf;
-    const uint32_t kst = my_ring + uint32_t(i % kStages) * 2 * kGroup, vst = kst + kGroup;
-    // K: tokens r and r + 8, dims [kDim / 4 * c, ..); V: tokens 2c, 2c + 1, 2c + 8, 2c + 9,
-    // dims [kDim / 8 * r, ..)
-    uint32_t kk[2][kDim / 16], vv[4][kDim / 32];
+    const int tok = first + i * kStepTokens;
+    float s[kG][NT][4], lv[kG];
+    bool gone[kG];   // groups without tokens, or of no page
+    bool masked = tok + 16 * kG > t_range || tok + 16 * kG > vis_all;
+    bool cut = tok + 16 * kG > rq.kv;
+    uint32_t st[kG];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int g = 0; g < kG; ++g) {
+      st[g] = my_ring + uint32_t(i % kStages) * kStage + g * 2 * kGroup;
+      // K: tokens r and r + 8, dims [kDim / 4 * c, ..)
+      uint32_t kk[2][kDim / 16];
 #pragma unroll
-      for (int j = 0; j < kDim / 64; ++j)
-        lds<4>(kst + place<kDim>(r + 8 * t, c * (kDim / 64) + j), &kk[t][4 * j]);
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int token = 2 * c + (t & 1) + 8 * (t >> 1);
-      if constexpr (kDim == 128)
-        lds<4>(vst + place<kDim>(token, r), vv[t]);
-      else
-        lds<2>(vst + place<kDim>(token, r >> 1) + 8 * (r & 1), vv[t]);
-    }
-    // V of tokens past the request's end may be anything, NaN codes included: zero
-    if (bad || tok + 16 > rq.kv) {
+        for (int j = 0; j < kDim / 64; ++j)
+          lds<4>(st[g] + place<kDim>(r + 8 * t, c * (kDim / 64) + j), &kk[t][4 * j]);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (bad || tok + 2 * c + (t & 1) + 8 * (t >> 1) >= rq.kv) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < kDim / 32; ++j) vv[t][j] = 0;
-        }
+        for (int j = 0; j < 4; ++j) s[g][nt][j] = 0.0f;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) {
+        uint32_t a0, a1, a2, a3;
+        e4m3_f16(kk[0][ks], a0, a2);
+        e4m3_f16(kk[1][ks], a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(s[g][nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
       }
     }
-    float s[NT][4];
+    bool raise = false;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      const float ks_page = __shfl_sync(0xFFFFFFFFu, win.ks, (i * kG + g) & 31);
+      lv[g] = __shfl_sync(0xFFFFFFFFu, win.lv, (i * kG + g) & 31);
+      gone[g] = ks_page == kNegInf;
+      masked |= gone[g];
+      cut |= gone[g];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float f = qs[nt][j] * ks_page;
+          s[g][nt][j] *= f;
+          s[g][nt][2 + j] *= f;
+        }
+    }
+    if (masked) {
+#pragma unroll
+      for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int left = (gone[g] ? 0 : min(vis[nt][j], t_range)) - tok - 16 * g - r;
+            if (left <= 0) s[g][nt][j] = kNegInf;
+            if (left <= 8) s[g][nt][2 + j] = kNegInf;
+          }
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
+      for (int j = 0; j < 2; ++j) {
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-      uint32_t a0, a1, a2, a3;
-      e4m3_f16(kk[0][ks], a0, a2);
-      e4m3_f16(kk[1][ks], a1, a3);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][ks][0], qf[nt][ks][1]);
-    }
-    const bool masked = bad || tok + 16 > t_range || tok + 16 > vis_all;
-    bool raise = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float f = qs[nt][i] * ks_page;
-        s[nt][i] *= f;
-        s[nt][2 + i] *= f;
-        if (masked) {
-          const int lim = bad ? 0 : min(vis[nt][i], t_range);
-          if (tok + r >= lim) s[nt][i] = kNegInf;
-          if (tok + r + 8 >= lim) s[nt][2 + i] = kNegInf;
-        }
-        const float top = fmaxf(s[nt][i], s[nt][2 + i]);
-        raise |= top > m[nt][i] + kLazy || top + lv > mv[nt][i] + kLazy;
+        for (int g = 0; g < kG; ++g)
+          raise |= fmaxf(s[g][nt][j], s[g][nt][2 + j]) > fminf(lim[nt][j], limv[nt][j] - lv[g]);
       }
-    }
     if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float top = fmaxf(s[nt][i], s[nt][2 + i]);
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-          const float mn = fmaxf(m[nt][i], top), mvn = fmaxf(mv[nt][i], top + lv);
-          if (mn > m[nt][i]) l[nt][i] *= exp2_approx(m[nt][i] - mn);
-          const float f = mvn > mv[nt][i] ? exp2_approx(mv[nt][i] - mvn) : 1.0f;
-          m[nt][i] = mn;
-          mv[nt][i] = mvn;
+        for (int j = 0; j < 2; ++j) {
+          float top = kNegInf, topv = kNegInf;
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            const float x = fmaxf(s[g][nt][j], s[g][nt][2 + j]);
+            top = fmaxf(top, x);
+            topv = fmaxf(topv, x + lv[g]);
+          }
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            topv = fmaxf(topv, __shfl_xor_sync(0xFFFFFFFFu, topv, o));
+          }
+          // (-inf stays: such a row has seen nothing)
+          const float was = lim[nt][j] - kLazy, wasv = limv[nt][j] - kLazy;
+          const float now = fmaxf(was, top), nowv = fmaxf(wasv, topv);
+          float f = 1.0f;
+          if (now > was) {
+            l[nt][j] *= exp2_approx(was - now);
+            base[nt][j] = now;
+            lim[nt][j] = now + kLazy;
+          }
+          if (nowv > wasv) {
+            f = exp2_approx(wasv - nowv);
+            basev[nt][j] = nowv - kBias;
+            limv[nt][j] = nowv + kLazy;
+          }
 #pragma unroll
           for (int t = 0; t < kTiles; ++t) {
-            o[nt][t][i] *= f;
-            o[nt][t][2 + i] *= f;
+            o[nt][t][j] *= f;
+            o[nt][t][2 + j] *= f;
           }
         }
     }
-    uint32_t pb[NT][2];
+    uint32_t pb[kG][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float w[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float base = m[nt][i] == kNegInf ? 0.0f : m[nt][i];
-        const float basev = mv[nt][i] == kNegInf ? 0.0f : mv[nt][i] - lv - kBias;
-        l[nt][i] += exp2_approx(s[nt][i] - base) + exp2_approx(s[nt][2 + i] - base);
-        w[i] = lv == kNegInf ? 0.0f : exp2_approx(s[nt][i] - basev);
-        w[2 + i] = lv == kNegInf ? 0.0f : exp2_approx(s[nt][2 + i] - basev);
+      for (int g = 0; g < kG; ++g) {
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          l[nt][j & 1] += exp2_approx(s[g][nt][j] - base[nt][j & 1]);
+          // lv = -inf (a scale of 0) gives 0
+          w[j] = exp2_approx(s[g][nt][j] + (lv[g] - basev[nt][j & 1]));
+        }
+        pb[g][nt][0] = transpose8x8(f16x2_rn(w[0], w[1]));
+        pb[g][nt][1] = transpose8x8(f16x2_rn(w[2], w[3]));
       }
-      pb[nt][0] = transpose8x8(f16x2_rn(w[0], w[1]));
-      pb[nt][1] = transpose8x8(f16x2_rn(w[2], w[3]));
     }
 #pragma unroll
-    for (int j = 0; j < kDim / 32; ++j) {
-      // words j of four tokens: dims 4 j .. 4 j + 3 of the lane's, two O tiles
-      const uint32_t x0 = prmt(vv[0][j], vv[1][j], 0x5140), x1 = prmt(vv[0][j], vv[1][j], 0x7362);
-      const uint32_t y0 = prmt(vv[2][j], vv[3][j], 0x5140), y1 = prmt(vv[2][j], vv[3][j], 0x7362);
-      uint32_t a0, a1, a2, a3;
-      e4m3_f16(x0, a0, a1);
-      e4m3_f16(y0, a2, a3);
+    for (int g = 0; g < kG; ++g) {
+      // V: tokens 2c, 2c + 1, 2c + 8, 2c + 9, dims [kDim / 8 * r, ..)
+      uint32_t vv[4][kDim / 32];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * j], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-      e4m3_f16(x1, a0, a1);
-      e4m3_f16(y1, a2, a3);
+      for (int t = 0; t < 4; ++t) {
+        const int token = 2 * c + (t & 1) + 8 * (t >> 1);
+        if constexpr (kDim == 128)
+          lds<4>(st[g] + kGroup + place<kDim>(token, r), vv[t]);
+        else
+          lds<2>(st[g] + kGroup + place<kDim>(token, r >> 1) + 8 * (r & 1), vv[t]);
+        // past the request's end (or in no page) it may be anything, NaN codes included: zero
+        if (cut && (gone[g] || tok + 16 * g + token >= rq.kv)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        mma_f16(o[nt][2 * j + 1], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+          for (int j = 0; j < kDim / 32; ++j) vv[t][j] = 0;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kDim / 32; ++j) {
+        // words j of four tokens: dims 4 j .. 4 j + 3 of the lane's, two O tiles
+        const uint32_t x0 = prmt(vv[0][j], vv[1][j], 0x5140);
+        const uint32_t x1 = prmt(vv[0][j], vv[1][j], 0x7362);
+        const uint32_t y0 = prmt(vv[2][j], vv[3][j], 0x5140);
+        const uint32_t y1 = prmt(vv[2][j], vv[3][j], 0x7362);
+        uint32_t a0, a1, a2, a3;
+        e4m3_f16(x0, a0, a1);
+        e4m3_f16(y0, a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(o[nt][2 * j], a0, a1, a2, a3, pb[g][nt][0], pb[g][nt][1]);
+        e4m3_f16(x1, a0, a1);
+        e4m3_f16(y1, a2, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma_f16(o[nt][2 * j + 1], a0, a1, a2, a3, pb[g][nt][0], pb[g][nt][1]);
+      }
     }
   };
 
-  Window cur = load_scales(0, load_pages(0)), nxt = cur;
-  int next_page = load_pages(32);
+  constexpr int kWin = 32 / kG;   // steps of a window
+  Window cur = load_window(0, first_page), nxt = cur;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) issue(i, cur);
-  for (int i = 0; i < n_groups; ++i) {
-    // the window of the groups that are copied runs kStages - 1 ahead of the computed ones'
-    if ((i & 31) == 16) nxt = load_scales((i & ~31) + 32, next_page);
-    if ((i & 31) == 0 && i > 0) {
+  for (int i = 0; i < n_steps; ++i) {
+    // the window of the steps that are copied runs kStages - 1 ahead of the computed ones'
+    if (i % kWin == kWin / 2) nxt = load_window((i / kWin + 1) * 32, next_page);
+    if (i % kWin == 0 && i > 0) {
       cur = nxt;
-      next_page = load_pages(i + 32);
+      next_page = load_pages((i / kWin + 1) * 32);
     }
     copies_wait<kStages - 2>();
-    __syncwarp();   // group i is there for every lane, and stage i - 1 is read by every lane
+    __syncwarp();   // step i is there for every lane, and stage i - 1 is read by every lane
     const int ahead = i + kStages - 1;
-    issue(ahead, (ahead >> 5) == (i >> 5) ? cur : nxt);
+    issue(ahead, ahead / kWin == i / kWin ? cur : nxt);
     compute(i, cur);
   }
   copies_wait<0>();
@@ -394,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
       l[nt][i] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][i], 16);
       const int row = 8 * nt + 2 * c + i;
       if (r == 0) {
-        sm[warp][0][row] = m[nt][i];
-        sm[warp][1][row] = mv[nt][i];
+        sm[warp][0][row] = lim[nt][i] == kNegInf ? kNegInf : base[nt][i];
+        sm[warp][1][row] = limv[nt][i] == kNegInf ? kNegInf : basev[nt][i];
         sm[warp][2][row] = l[nt][i];
       }
 #pragma unroll
@@ -406,6 +489,9 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
     }
   __syncthreads();
   constexpr int kPer = kDim / 16;   // 16 lanes a row
+  // a cluster's parts, behind the warps' rows
+  float (*part)[kDim + 4] = reinterpret_cast<float (*)[kDim + 4]>(&so[kWarps][0][0]);
+  const int d0 = (tid & 15) * kPer;
   for (int row = tid >> 4; row < kRows; row += kThreads / 16) {
     const int rho = rho0 + row;
     if (rho >= rows) break;
@@ -415,66 +501,143 @@ __global__ void __launch_bounds__(kThreads, 3) decode_kernel(const Args a) {
       mt = fmaxf(mt, sm[w][0][row]);
       mvt = fmaxf(mvt, sm[w][1][row]);
     }
-    const float base = mt == kNegInf ? 0.0f : mt, basev = mvt == kNegInf ? 0.0f : mvt;
+    const float top = mt == kNegInf ? 0.0f : mt, topv = mvt == kNegInf ? 0.0f : mvt;
     float sum = 0.0f, f[kWarps];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      sum += sm[w][2][row] * exp2_approx(sm[w][0][row] - base);
-      f[w] = exp2_approx(sm[w][1][row] - basev);
+      sum += sm[w][2][row] * exp2_approx(sm[w][0][row] - top);
+      f[w] = exp2_approx(sm[w][1][row] - topv);
     }
     // 2^(weights' maximum - maximum) / sum; a row that sees nothing is zero
-    const float norm = sum == 0.0f ? 0.0f : exp2f(basev - kBias - base) / sum;
-    const float lse2 = sum == 0.0f ? kNegInf : base + log2f(sum);
+    const float norm = sum == 0.0f ? 0.0f : exp2f(topv - top) / sum;
+    const float lse2 = sum == 0.0f ? kNegInf : top + log2f(sum);
     float v[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int d = (tid & 15) * kPer + i;
+      const int d = d0 + i;
       float x = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) x = fmaf(so[w][row][d], f[w], x);
       v[i] = x * norm;
     }
-    store_row<kPer, kDim>(a, rq, h, rho, split, used, (tid & 15) * kPer, v, lse2, (tid & 15) == 0);
+    if (used > 1 && a.cluster) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) part[row][d0 + i] = v[i];
+      if (d0 == 0) part[row][kDim] = lse2;
+    } else {
+      store_row<kPer, kDim>(a, rq, h, rho, split, used, d0, v, lse2, d0 == 0);
+    }
   }
+  if (!a.cluster) return;
+  // the ranges of a cluster: row by row through distributed shared memory, in order
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  if (used > 1) {
+    for (int row = split + (tid >> 4) * used; row < kRows && rho0 + row < rows;
+         row += kThreads / 16 * used) {
+      const float* from[kMaxCluster];
+      float lse[kMaxCluster], top = kNegInf, sum = 0.0f, v[kPer];
+#pragma unroll
+      for (int s = 0; s < kMaxCluster; ++s) {
+        lse[s] = kNegInf;
+        if (s < used) {
+          from[s] = cluster.map_shared_rank(part[row], s);
+          lse[s] = from[s][kDim];
+          top = fmaxf(top, lse[s]);
+        }
+      }
+      const float base = top == kNegInf ? 0.0f : top;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kMaxCluster; ++s) {
+        if (s < used) {
+          const float w = exp2f(lse[s] - base);
+          sum += w;
+#pragma unroll
+          for (int i = 0; i < kPer; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(from[s] + d0 + i);
+            v[i] = fmaf(w, x.x, v[i]);
+            v[i + 1] = fmaf(w, x.y, v[i + 1]);
+            v[i + 2] = fmaf(w, x.z, v[i + 2]);
+            v[i + 3] = fmaf(w, x.w, v[i + 3]);
+          }
+        }
+      }
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] *= inv;
+      store_row<kPer, kDim>(a, rq, h, rho0 + row, 0, 1, d0, v,
+                            sum == 0.0f ? kNegInf : base + log2f(sum), d0 == 0);
+    }
+  }
+  cluster.sync();   // the others read this CTA's part until here
 }
 
-// Joins the ranges of requests that were split: one warp a row, ranges in order.
-template <int kDim>
+// Joins the ranges of requests that were split.  WPR warps a row take its ranges in turn,
+// eight loads in flight each; their sums are added in order.
+template <int kDim, int WPR>
 __global__ void __launch_bounds__(kThreads) join_kernel(const Args a) {
-  constexpr int kPer = kDim / 32;
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  constexpr int kPer = kDim / 32, kJoined = kWarps / WPR;   // rows of a CTA
+  __shared__ float rows_of[WPR][kJoined][kDim + 1];
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = warp / kJoined;
   pdl_wait();
   pdl_trigger();
   const Request rq = request(a, b, false);
   const int used = splits_of(a, rq.kv);
-  const int n = int(blockIdx.x) * kWarps + (threadIdx.x >> 5);  // (token, head) of the request
-  if (used <= 1 || n >= rq.nq * a.q_heads) return;
+  if (used <= 1) return;
+  const int n = int(blockIdx.x) * kJoined + warp % kJoined;   // (token, head) of the request
+  const bool live = n < rq.nq * a.q_heads;
   const int64_t row = int64_t(rq.q0) * a.q_heads + n;
   const int64_t plane = int64_t(a.tq) * a.q_heads;
-  float top = kNegInf;
-  for (int s = lane; s < used; s += 32) top = fmaxf(top, a.part_lse[s * plane + row]);
+  float top = kNegInf, sum = 0.0f, v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
+  if (live)
+    for (int s = lane; s < used; s += 32) top = fmaxf(top, a.part_lse[s * plane + row]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   const float base = top == kNegInf ? 0.0f : top;
-  float sum = 0.0f, v[kPer];
+  if (live) {
+    for (int s0 = g; s0 < used; s0 += 8 * WPR) {
+      float w[8], x[8][kPer];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
-  for (int s = 0; s < used; ++s) {
-    const float w = exp2f(a.part_lse[s * plane + row] - base);
-    const float* p = a.part_o + (s * plane + row) * kDim + lane * kPer;
-    sum += w;
-    if constexpr (kPer == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(p);
-      v[0] = fmaf(w, x.x, v[0]);
-      v[1] = fmaf(w, x.y, v[1]);
-      v[2] = fmaf(w, x.z, v[2]);
-      v[3] = fmaf(w, x.w, v[3]);
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(p);
-      v[0] = fmaf(w, x.x, v[0]);
-      v[1] = fmaf(w, x.y, v[1]);
+      for (int j = 0; j < 8; ++j) {
+        const int s = s0 + j * WPR;
+        w[j] = s < used ? a.part_lse[s * plane + row] : kNegInf;
+        const float* p = a.part_o + (min(s, used - 1) * plane + row) * kDim + lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 q = *reinterpret_cast<const float4*>(p);
+          x[j][0] = q.x, x[j][1] = q.y, x[j][2] = q.z, x[j][3] = q.w;
+        } else {
+          const float2 q = *reinterpret_cast<const float2*>(p);
+          x[j][0] = q.x, x[j][1] = q.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float f = exp2f(w[j] - base);
+        sum += f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] = fmaf(f, x[j][i], v[i]);
+      }
     }
   }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) rows_of[g][warp % kJoined][lane * kPer + i] = v[i];
+    if (lane == 0) rows_of[g][warp % kJoined][kDim] = sum;
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int j = 1; j < WPR; ++j) {
+      sum += rows_of[j][warp % kJoined][kDim];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] += rows_of[j][warp % kJoined][lane * kPer + i];
+    }
+  }
+  if (!live) return;
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int64_t tok = rq.q0 + n / a.q_heads;
   uint16_t* dst = a.out + tok * a.out_stride + int64_t(n % a.q_heads) * kDim + lane * kPer;
@@ -489,27 +652,40 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args a) {
     a.lse[row] = sum == 0.0f ? kNegInf : (base + log2f(sum)) * 0.6931471805599453f;
 }
 
-template <int kDim>
-static cudaError_t launch_dim(const Args& a, const Kv8Plan& p, int32_t batch, int32_t max_q,
-                              cudaStream_t st) {
-  const dim3 grid(unsigned(p.n_splits) * unsigned(p.row_tiles), unsigned(a.kv_heads),
-                  unsigned(batch));
-  cudaError_t e = cudaSuccess;
+template <int kDim, int NT>
+cudaError_t launch_decode(const Args& a, dim3 grid, cudaStream_t st) {
   // the rings, or the joined rows if they are larger
-  constexpr size_t kRing = size_t(kWarps) * kStages * 2 * 16 * kDim;
-  constexpr size_t kSmem = std::max(kRing, size_t(kWarps) * 16 * (kDim + 4) * sizeof(float));
-  if (p.rows == 8) {
-    e = allow_smem<decode_kernel<kDim, 1>>(kSmem);
-    if (e == cudaSuccess)
-      e = launch_pdl(decode_kernel<kDim, 1>, grid, dim3(kThreads), kSmem, st, a);
-  } else {
-    e = allow_smem<decode_kernel<kDim, 2>>(kSmem);
-    if (e == cudaSuccess)
-      e = launch_pdl(decode_kernel<kDim, 2>, grid, dim3(kThreads), kSmem, st, a);
-  }
-  if (e != cudaSuccess || p.n_splits == 1) return e;
+  constexpr size_t kRing = size_t(kWarps) * kStages * kGroups<kDim, NT> * 2 * 16 * kDim;
+  constexpr size_t kSmem =
+      std::max(kRing, size_t(kWarps + 1) * 8 * NT * (kDim + 4) * sizeof(float));
+  // Clusters get shared memory for three CTAs an SM, as the number of ranges assumes: where a
+  // fourth fits, they are packed onto some SMs and leave others idle (16 x 8500 tokens, 4
+  // heads: 34 us against 30).
+  const size_t smem = a.cluster ? std::max(kSmem, size_t(72) << 10) : kSmem;
+  const cudaError_t e = allow_smem<decode_kernel<kDim, NT>>(std::max(kSmem, size_t(72) << 10));
+  if (e != cudaSuccess) return e;
+  return launch_pdl_cluster(decode_kernel<kDim, NT>, grid, dim3(1, 1, a.cluster ? a.n_splits : 1),
+                            dim3(kThreads), smem, st, a);
+}
+
+template <int kDim>
+cudaError_t launch_dim(const Args& a, const Kv8Plan& p, int32_t batch, int32_t max_q,
+                              cudaStream_t st) {
+  const dim3 grid(unsigned(a.kv_heads) * unsigned(p.row_tiles), unsigned(batch),
+                  unsigned(p.n_splits));
+  cudaError_t e = cudaSuccess;
+  if (p.rows == 8)
+    e = launch_decode<kDim, 1>(a, grid, st);
+  else
+    e = launch_decode<kDim, 2>(a, grid, st);
+  if (e != cudaSuccess || p.n_splits == 1 || a.cluster) return e;
+  // a warp a row for up to 8 ranges, a CTA a row beyond
   const int64_t rows = int64_t(max_q) * a.q_heads;
-  return launch_pdl(join_kernel<kDim>, dim3(unsigned((rows + kWarps - 1) / kWarps), unsigned(batch)),
+  if (p.n_splits <= 8)
+    return launch_pdl(join_kernel<kDim, 1>,
+                      dim3(unsigned((rows + kWarps - 1) / kWarps), unsigned(batch)),
+                      dim3(kThreads), 0, st, a);
+  return launch_pdl(join_kernel<kDim, kWarps>, dim3(unsigned(rows), unsigned(batch)),
                     dim3(kThreads), 0, st, a);
 }
 
@@ -522,20 +698,30 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   const int64_t rows = int64_t(d.max_q) * group;
   p.rows = rows <= 8 ? 8 : 16;
   p.row_tiles = int32_t((rows + p.rows - 1) / p.rows);
-  // ranges: enough CTAs for a few on every SM, none shorter than 256 tokens
+  // Ranges, none shorter than 128 tokens.  Few units: as many as fill one wave of three CTAs
+  // an SM (2 x 131072 tokens, 8 heads: 86 us; 93 for four an SM, 107 in 2.7 waves), or the 8
+  // of a cluster where that keeps a range below 512 tokens (1500 tokens, 24 heads: 6.9 us
+  // against 8.3).  Many units: enough ranges for three waves of four CTAs an SM, because
+  // lengths differ (64 ragged requests, 8 heads: 90 us in four ranges, 96 in two, 105 in one),
+  // until there are two waves of units (200 requests: 76 us whole, 80 in two ranges).
   const int64_t units = int64_t(d.batch) * d.kv_heads * p.row_tiles;
-  const int64_t want = (int64_t(d.sm_count) * 8 + units - 1) / units;
-  const int64_t most = (int64_t(d.max_kv) + 255) / 256;
-  int64_t n = want < most ? want : most;
-  if (n < 1) n = 1;
-  if (n > NVFP4_KV8_MAX_SPLITS) n = NVFP4_KV8_MAX_SPLITS;
+  const int64_t sms = d.sm_count, wave = sms * 3;
+  int64_t n = units * 2 <= wave ? wave / units : units < sms * 8 ? (sms * 12 + units - 1) / units : 1;
+  n = std::min(n, (int64_t(d.max_kv) + 127) / 128);
+  if (n > kv8::kMaxCluster && d.max_kv <= kv8::kMaxCluster * 512) n = kv8::kMaxCluster;
+  n = std::max<int64_t>(1, std::min<int64_t>(n, NVFP4_KV8_MAX_SPLITS));
   const int64_t chunk = ((int64_t(d.max_kv) + n - 1) / n + 63) / 64 * 64;
   p.chunk = int32_t(chunk < 64 ? 64 : chunk);
   p.n_splits = int32_t((int64_t(d.max_kv) + p.chunk - 1) / p.chunk);
   if (p.n_splits < 1) p.n_splits = 1;
-  p.scratch = p.n_splits == 1 ? 0
-                              : size_t(p.n_splits) * size_t(d.tq) * size_t(d.q_heads) *
-                                    size_t(d.head_dim + 1) * sizeof(float);
+  // In one wave the ranges of a unit can be a cluster, which joins them without a second
+  // kernel (777 tokens, 24 heads: 5.9 us against 7.6); in several, CTAs that wait for their
+  // cluster hold up others (64 ragged requests: 121 us against 94).
+  p.cluster = p.n_splits > 1 && p.n_splits <= kv8::kMaxCluster && units * p.n_splits <= wave;
+  p.scratch = p.n_splits == 1 || p.cluster
+                  ? 0
+                  : size_t(p.n_splits) * size_t(d.tq) * size_t(d.q_heads) *
+                        size_t(d.head_dim + 1) * sizeof(float);
   return p;
 }
 
@@ -569,6 +755,7 @@ cudaError_t launch_kv8_attention(const LaunchKv8Attn& d, cudaStream_t st) {
   a.scale_log2 = d.scale_log2;
   a.chunk = p.chunk;
   a.n_splits = p.n_splits;
+  a.cluster = p.cluster;
   a.part_o = static_cast<float*>(d.scratch);
   a.part_lse = a.part_o + int64_t(p.n_splits) * d.tq * d.q_heads * d.head_dim;
   a.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d.ws) + kWsStatus);
