@@ -51,11 +51,14 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "kernels.h"
+#include "tc.cuh"
 
 #include <atomic>
 
 namespace nvfp4 {
 namespace attn {
+
+using namespace tc;
 
 constexpr int kD = 128;                   // head_dim
 constexpr int kBQ = 128;                  // queries per query tile (tensor-memory lanes)
@@ -68,7 +71,6 @@ constexpr int kDecWarp0 = kMmaWarp + 1;   // 9
 constexpr int kDecWarps = 8;
 constexpr int kThreads = (kDecWarp0 + kDecWarps) * 32;  // 544
 constexpr int kStages = 2;
-constexpr int kChunkBytes = 128 * 128;    // 128 rows x 64 bf16 (one K chunk of an operand)
 constexpr int kOpBytes = 2 * kChunkBytes;  // 128 rows x 128 bf16
 // shared memory map (offsets from a 1024-byte aligned base)
 constexpr int kOffQ = 0;                                 // + g * kOpBytes
@@ -88,6 +90,9 @@ constexpr uint32_t kSCol0 = 256;          // S_g (then P_g) at kSCol0 + 128 g
 // 10), both K-major, N >> 3 at bits 17-22, M >> 4 at bits 24-28.
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(kBK >> 3) << 17) |
                             (uint32_t(kBQ >> 4) << 24);
+// The P V product's descriptor: as kIdesc with B MN-major (bit 16): V is
+// stored [key][dim], dims contiguous.
+constexpr uint32_t kIdescPV = kIdesc | (1u << 16);
 constexpr float kLazyLog2 = 16.0f;         // largest probability kept before a rescale: 2^16
 
 struct AttnArgs {
@@ -103,199 +108,6 @@ struct AttnArgs {
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t slots[NVFP4_KV_MAX_WINDOW_SLOTS];
-};
-
-// ---------------------------------------------------------------- PTX wrappers
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ uint64_t globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(20000)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ void bar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-      : "memory");
-}
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups
-// 1024 bytes apart, descriptor version 1.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-// D (+)= A B^T, A and B in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
-      : "memory");
-}
-// Shared-memory matrix descriptor of an MN-major operand, 128-byte swizzle:
-// 8-row (K) groups 1024 bytes apart (SBO), 64-element MN chunks
-// kMnChunkBytes apart (LBO), descriptor version 1.
-#ifndef ATTN_V_LBO
-#define ATTN_V_LBO (128 * 128)
-#endif
-#ifndef ATTN_V_SBO
-#define ATTN_V_SBO 1024
-#endif
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr) {
-  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(ATTN_V_LBO >> 4) << 16) |
-         (uint64_t(ATTN_V_SBO >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-// The P V product's descriptor: as kIdesc with B MN-major (bit 16): V is
-// stored [key][dim], dims contiguous.
-constexpr uint32_t kIdescPV = kIdesc | (1u << 16);
-// D (+)= A B^T, A in tensor memory, B MN-major.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kIdescPV), "r"(acc)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-// The same load without its wait (pair with tmem_wait_ld).
-__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// Waits for every earlier tensor-memory load of the thread, then ties the
-// registers of both loads to the wait so that nothing reading them can be
-// scheduled before it.
-// max of three (sm_100's three-input form; NaN handling as fmaxf)
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-__device__ __forceinline__ void regs_after_wait(uint32_t (&r)[32]) {
-  asm volatile(
-      ""
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
-        "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
-        "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
-        "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r0)[32], uint32_t (&r1)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  regs_after_wait(r0);
-  regs_after_wait(r1);
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-               "r"(v.z), "r"(v.w)
-               : "memory");
-}
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-
-// Byte offset of 16-byte unit u (0..15: elements 8u..8u+7) of row r in a
-// 128-row operand tile of 128 bf16 per row, in the tensor core's K-major,
-// 128-byte-swizzled layout (two 64-element chunks of 16 KB).
-__device__ __forceinline__ uint32_t op_offset(uint32_t r, uint32_t u) {
-  return (u >> 3) * kChunkBytes + (r >> 3) * 1024 + (r & 7) * 128 + (((u & 7) ^ (r & 7)) << 4);
-}
-
-// 2^x with the hardware approximation (relative error about 2^-22; results
-// below 2^-126 flush to zero, which the softmax sums cannot notice).
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-struct Waiter {
-  uint64_t limit_ns;
-  volatile int* abort;
-  uint32_t* status;
-  // Wait for phase `parity` of `bar`; false if the CTA aborted or the wait ran out.
-  __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
-    if (bar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (true) {
-      if (*abort) return false;
-      if (bar_try_wait(bar, parity)) return true;
-      if (globaltimer() - t0 > limit_ns) {
-        record_status(status, NVFP4_ERR_TIMEOUT);
-        *abort = 1;
-        return false;
-      }
-    }
-  }
 };
 
 // Decoded bf16 of one 16-element block of K or V: token w of the window
@@ -523,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_attention_kernel(const Att
 #pragma unroll
         for (uint32_t ks = 0; ks < 8; ++ks)  // 16 dims a step: +32 bytes, next chunk after 4
           mma_ss(tmem + kSCol0 + 128 * g, qd + (ks >> 2) * (kChunkBytes >> 4) + 2 * (ks & 3),
-                 kd + (ks >> 2) * (kChunkBytes >> 4) + 2 * (ks & 3), ks != 0);
+                 kd + (ks >> 2) * (kChunkBytes >> 4) + 2 * (ks & 3), kIdesc, ks != 0);
         tc_commit(bar_s_full + 8 * g);
       };
       // O_g += P_g(j) V_j, P from S_g's columns, V from ring stage j % 2
@@ -534,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_attention_kernel(const Att
         const uint32_t p_addr = tmem + kSCol0 + 128 * g;
 #pragma unroll
         for (uint32_t ks = 0; ks < 8; ++ks)  // 16 keys a step: 8 columns of P, two 8-key groups of V
-          mma_ts(tmem + kOCol0 + 128 * g, p_addr + 8 * ks, vd + ks * (2048 >> 4), (j | ks) != 0);
+          mma_ts(tmem + kOCol0 + 128 * g, p_addr + 8 * ks, vd + ks * (2048 >> 4), kIdescPV,
+                 (j | ks) != 0);
         tc_commit(bar_pv_done + 8 * g);
         return true;
       };

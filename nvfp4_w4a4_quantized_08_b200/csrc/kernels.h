@@ -165,6 +165,7 @@ struct LaunchKv8Attn {
   int sm_count;
 };
 struct Kv8Plan {
+  bool chunked;       // the tensor-core kernel of many rows
   int32_t rows;       // rows of a tile
   int32_t row_tiles;  // tiles of a request's rows
   int32_t chunk, n_splits;

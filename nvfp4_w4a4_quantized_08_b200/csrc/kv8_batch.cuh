@@ -30,6 +30,7 @@ struct Args {
   float* part_o;           // [n_splits][tq][q_heads][dim]
   float* part_lse;         // [n_splits][tq][q_heads], base 2
   uint32_t* status;
+  uint64_t wait_limit_ns;
 };
 
 struct Request {
@@ -99,4 +100,8 @@ __device__ __forceinline__ void store_row(const Args& a, const Request& r, int h
 }
 
 }  // namespace kv8
+
+cudaError_t launch_kv8_chunk(const kv8::Args& a, int32_t head_dim, int32_t row_tiles, int32_t batch,
+                             cudaStream_t st);
+
 }  // namespace nvfp4

@@ -669,24 +669,30 @@ cudaError_t launch_decode(const Args& a, dim3 grid, cudaStream_t st) {
 }
 
 template <int kDim>
-cudaError_t launch_dim(const Args& a, const Kv8Plan& p, int32_t batch, int32_t max_q,
-                              cudaStream_t st) {
-  const dim3 grid(unsigned(a.kv_heads) * unsigned(p.row_tiles), unsigned(batch),
-                  unsigned(p.n_splits));
-  cudaError_t e = cudaSuccess;
-  if (p.rows == 8)
-    e = launch_decode<kDim, 1>(a, grid, st);
-  else
-    e = launch_decode<kDim, 2>(a, grid, st);
-  if (e != cudaSuccess || p.n_splits == 1 || a.cluster) return e;
+cudaError_t launch_join(const Args& a, int32_t batch, int32_t max_q, cudaStream_t st) {
   // a warp a row for up to 8 ranges, a CTA a row beyond
   const int64_t rows = int64_t(max_q) * a.q_heads;
-  if (p.n_splits <= 8)
+  if (a.n_splits <= 8)
     return launch_pdl(join_kernel<kDim, 1>,
                       dim3(unsigned((rows + kWarps - 1) / kWarps), unsigned(batch)),
                       dim3(kThreads), 0, st, a);
   return launch_pdl(join_kernel<kDim, kWarps>, dim3(unsigned(rows), unsigned(batch)),
                     dim3(kThreads), 0, st, a);
+}
+
+template <int kDim>
+cudaError_t launch_dim(const Args& a, const Kv8Plan& p, int32_t batch, int32_t max_q,
+                       cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  if (p.chunked) {
+    e = launch_kv8_chunk(a, kDim, p.row_tiles, batch, st);
+  } else {
+    const dim3 grid(unsigned(a.kv_heads) * unsigned(p.row_tiles), unsigned(batch),
+                    unsigned(p.n_splits));
+    e = p.rows == 8 ? launch_decode<kDim, 1>(a, grid, st) : launch_decode<kDim, 2>(a, grid, st);
+  }
+  if (e != cudaSuccess || p.n_splits == 1 || a.cluster) return e;
+  return launch_join<kDim>(a, batch, max_q, st);
 }
 
 }  // namespace kv8
@@ -696,7 +702,8 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   Kv8Plan p;
   const int32_t group = d.q_heads / d.kv_heads;
   const int64_t rows = int64_t(d.max_q) * group;
-  p.rows = rows <= 8 ? 8 : 16;
+  p.chunked = rows > 16;
+  p.rows = p.chunked ? 256 : rows <= 8 ? 8 : 16;
   p.row_tiles = int32_t((rows + p.rows - 1) / p.rows);
   // Ranges, none shorter than 128 tokens.  Few units: as many as fill one wave of three CTAs
   // an SM (2 x 131072 tokens, 8 heads: 86 us; 93 for four an SM, 107 in 2.7 waves), or the 8
@@ -709,15 +716,19 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   int64_t n = units * 2 <= wave ? wave / units : units < sms * 8 ? (sms * 12 + units - 1) / units : 1;
   n = std::min(n, (int64_t(d.max_kv) + 127) / 128);
   if (n > kv8::kMaxCluster && d.max_kv <= kv8::kMaxCluster * 512) n = kv8::kMaxCluster;
+  // Chunks: ranges only where the row tiles leave half of the SMs without a CTA.
+  if (p.chunked)
+    n = units * 2 <= sms ? std::min(sms / units, (int64_t(d.max_kv) + 511) / 512) : 1;
   n = std::max<int64_t>(1, std::min<int64_t>(n, NVFP4_KV8_MAX_SPLITS));
-  const int64_t chunk = ((int64_t(d.max_kv) + n - 1) / n + 63) / 64 * 64;
-  p.chunk = int32_t(chunk < 64 ? 64 : chunk);
+  const int64_t whole = p.chunked ? 128 : 64;   // a range is whole tiles of tokens
+  const int64_t chunk = ((int64_t(d.max_kv) + n - 1) / n + whole - 1) / whole * whole;
+  p.chunk = int32_t(std::max(chunk, whole));
   p.n_splits = int32_t((int64_t(d.max_kv) + p.chunk - 1) / p.chunk);
   if (p.n_splits < 1) p.n_splits = 1;
   // In one wave the ranges of a unit can be a cluster, which joins them without a second
   // kernel (777 tokens, 24 heads: 5.9 us against 7.6); in several, CTAs that wait for their
   // cluster hold up others (64 ragged requests: 121 us against 94).
-  p.cluster = p.n_splits > 1 && p.n_splits <= kv8::kMaxCluster && units * p.n_splits <= wave;
+  p.cluster = !p.chunked && p.n_splits > 1 && p.n_splits <= kv8::kMaxCluster && units * p.n_splits <= wave;
   p.scratch = p.n_splits == 1 || p.cluster
                   ? 0
                   : size_t(p.n_splits) * size_t(d.tq) * size_t(d.q_heads) *
@@ -759,6 +770,7 @@ cudaError_t launch_kv8_attention(const LaunchKv8Attn& d, cudaStream_t st) {
   a.part_o = static_cast<float*>(d.scratch);
   a.part_lse = a.part_o + int64_t(p.n_splits) * d.tq * d.q_heads * d.head_dim;
   a.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(d.ws) + kWsStatus);
+  a.wait_limit_ns = d.wait_limit_ns;
   return d.head_dim == 64 ? kv8::launch_dim<64>(a, p, d.batch, d.max_q, st)
                           : kv8::launch_dim<128>(a, p, d.batch, d.max_q, st);
 }
