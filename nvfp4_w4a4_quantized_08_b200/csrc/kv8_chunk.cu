@@ -9,16 +9,19 @@
 // tiles of 128) of one request and KV head and a range of its tokens:
 //   warps 0..7   softmax: warpgroup g owns row tile g, one row a thread.  A row's 128
 //                scores of a tile are read from tensor memory once, into registers
-//                (184 a thread, moved over from the other warps by setmaxnreg); the
+//                (200 a thread, moved over from the other warps by setmaxnreg); the
 //                probabilities go back as bf16, in two halves, so that P V starts on the
 //                first while the second is computed.
-//   warps 8..11  decoders: E4M3 codes of the next tile, loaded one tile ahead, to bf16 K and
-//                V operands in 128-byte-swizzled shared memory (two stages).  A code is
-//                shifted into place and multiplied by 2^120, two at a time: exact.  The
-//                order of 8 dims is the one in which that needs no byte permutes (0 2 1 3 4
-//                6 5 7); Q is stored in the same order, the output is read in it.
+//   warps 8..11  decoders: E4M3 codes -> bf16 K and V operands in 128-byte-swizzled shared
+//                memory (two stages each).  A code is shifted into place and multiplied by
+//                2^120, two at a time: exact.  The order of 8 dims is the one in which that
+//                needs no byte permutes (0 2 1 3 4 6 5 7); Q is stored in the same order, the
+//                output is read in it.  Every byte decodes to something finite, so tokens past
+//                the end need no clearing: their probabilities are 0.
 //   warp 12      issues the MMAs: ... PV0_j, S0_{j+1}, PV1_j, S1_{j+1}, PV0_{j+1} ..., so
 //                the tensor core works on one row tile while the other's softmax runs.
+//   warp 13      copies the codes of a tile ahead (one bulk copy for the 16 tokens of a group,
+//                which share a page).
 // Tensor memory (512 columns): O0, O1, S0, S1; P_g takes S_g's place.
 //
 // The codes go into the products without their page scales.  Scores of a group of 16 tokens
@@ -49,9 +52,12 @@ constexpr int kSoftWarps = 8;              // warps 0..7
 constexpr int kDecWarps = 4;               // warps 8..11
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
 constexpr int kThreads = 512;              // four warpgroups; the last has the MMA warp only
-constexpr int kStages = 2;
+constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kStages = 2;                 // decoded tiles of K, and of V
+constexpr int kMetaStages = 4;             // page scales: read later than K
+constexpr int kMetaFloats = 3 * kGroups;
 // registers a thread at launch, and after the warpgroups have shared them out anew
-constexpr int kLaunchRegs = 128, kSoftRegs = 184, kDecRegs = 104, kMmaRegs = 40;
+constexpr int kLaunchRegs = 128, kSoftRegs = 200, kDecRegs = 56, kMmaRegs = 56;
 static_assert(2 * kSoftRegs + kDecRegs + kMmaRegs == 4 * kLaunchRegs, "register split");
 static_assert(kThreads * kLaunchRegs <= 65536, "registers of an SM");
 constexpr uint32_t kTmemCols = 512;
@@ -63,10 +69,14 @@ struct Layout {
   static constexpr int kChunks = kD / 64;
   static constexpr int kOp = kChunks * kChunkBytes;        // 128 rows x kD bf16
   static constexpr int kQ = 0, kK = kTiles * kOp, kV = kK + kStages * kOp;
-  static constexpr int kMeta = kV + kStages * kOp;         // [stage][3][group] floats
-  static constexpr int kBar = kMeta + kStages * 3 * kGroups * 4;
-  // q_ready[2], kv_full[2], kv_empty[2], s_full[2], p_ready[2][2], pv_done[2], o_full, drain
-  static constexpr int kNumBars = 2 * kTiles + 2 * kStages + 2 * kTiles + kTiles + 2;
+  static constexpr int kRaw = kD == 64 ? 3 : 1;            // tiles of codes ahead
+  static constexpr int kRawBytes = kKeys * kD;             // of one plane
+  static constexpr int kRawK = kV + kStages * kOp, kRawV = kRawK + kRaw * kRawBytes;
+  static constexpr int kMeta = kRawV + kRaw * kRawBytes;   // [stage][3][group] floats
+  static constexpr int kBar = kMeta + kMetaStages * kMetaFloats * 4;
+  // q[2], k_full, k_empty, v_full, v_empty [stage], s_full[2], p_ready[2][2], pv_done[2],
+  // meta_full[4], raw K full, empty, raw V full, empty [raw stage], o_full, drain
+  static constexpr int kNumBars = 2 + 4 * kStages + 2 + 4 + 2 + kMetaStages + 4 * kRaw + 2;
   static constexpr int kTmemPtr = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemPtr + 4;
   static constexpr int kBytes = kAbort + 4 + 1024;
@@ -116,12 +126,19 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                              ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar_q = sbase + L::kBar;                      // + 8 g
-  const uint32_t bar_kv_full = bar_q + 8 * kTiles;             // + 8 stage
-  const uint32_t bar_kv_empty = bar_kv_full + 8 * kStages;     // + 8 stage
-  const uint32_t bar_s_full = bar_kv_empty + 8 * kStages;      // + 8 g
+  const uint32_t bar_k_full = bar_q + 8 * kTiles;              // + 8 stage
+  const uint32_t bar_k_empty = bar_k_full + 8 * kStages;
+  const uint32_t bar_v_full = bar_k_empty + 8 * kStages;
+  const uint32_t bar_v_empty = bar_v_full + 8 * kStages;
+  const uint32_t bar_s_full = bar_v_empty + 8 * kStages;       // + 8 g
   const uint32_t bar_p_ready = bar_s_full + 8 * kTiles;        // + 16 g + 8 half
   const uint32_t bar_pv_done = bar_p_ready + 16 * kTiles;      // + 8 g
-  const uint32_t bar_o_full = bar_pv_done + 8 * kTiles;
+  const uint32_t bar_meta = bar_pv_done + 8 * kTiles;          // + 8 stage
+  const uint32_t bar_rk_full = bar_meta + 8 * kMetaStages;     // + 8 raw stage
+  const uint32_t bar_rk_empty = bar_rk_full + 8 * L::kRaw;
+  const uint32_t bar_rv_full = bar_rk_empty + 8 * L::kRaw;
+  const uint32_t bar_rv_empty = bar_rv_full + 8 * L::kRaw;
+  const uint32_t bar_o_full = bar_rv_empty + 8 * L::kRaw;
   const uint32_t bar_drain = bar_o_full + 8;
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + L::kTmemPtr);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kAbort);
@@ -141,8 +158,17 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       bar_init(bar_pv_done + 8 * g, 1);
     }
     for (int s = 0; s < kStages; ++s) {
-      bar_init(bar_kv_full + 8 * s, kDecWarps);
-      bar_init(bar_kv_empty + 8 * s, 1);
+      bar_init(bar_k_full + 8 * s, kDecWarps);
+      bar_init(bar_k_empty + 8 * s, 1);
+      bar_init(bar_v_full + 8 * s, kDecWarps);
+      bar_init(bar_v_empty + 8 * s, 1);
+    }
+    for (int s = 0; s < kMetaStages; ++s) bar_init(bar_meta + 8 * s, 1);
+    for (int s = 0; s < L::kRaw; ++s) {
+      bar_init(bar_rk_full + 8 * s, 1);
+      bar_init(bar_rk_empty + 8 * s, kDecWarps);
+      bar_init(bar_rv_full + 8 * s, 1);
+      bar_init(bar_rv_empty + 8 * s, kDecWarps);
     }
     bar_init(bar_o_full, 1);
     bar_init(bar_drain, 1);
@@ -205,16 +231,18 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) bar_arrive(bar_q + 8 * g);
       for (int j = 0; j < n_tiles; ++j) {
-        const int st = j % kStages;
-        // kv_full: the page scales that the decoders wrote (complete since S is)
-        ok = waiter.wait(bar_s_full + 8 * g, j & 1) &&
-             waiter.wait(bar_kv_full + 8 * st, (j / kStages) & 1);
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = __all_sync(0xFFFFFFFFu, waiter.wait(bar_meta + 8 * (j % kMetaStages),
+                                                 (j / kMetaStages) & 1));
+        if (!ok) break;
+        // per group: K scale times scale * log2 e; log2 of the V scale; 1 / V scale (0: no
+        // page, left out)
+        const float* ms = meta + (j % kMetaStages) * kMetaFloats;
+        float sc[kGroups];
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) sc[n] = ms[n];
+        ok = __all_sync(0xFFFFFFFFu, waiter.wait(bar_s_full + 8 * g, j & 1));
         if (!ok) break;
         tc_fence_after();
-        const float* sc = meta + st * 3 * kGroups;   // K scale times scale * log2 e
-        const float* lv = sc + kGroups;              // log2 of the V scale
-        const float* inv = lv + kGroups;             // 1 / V scale; 0: no page, left out
         uint32_t r[4][32];
         load_scores(s_addr, r);
         if (vis_min < (j + 1) * kKeys) {
@@ -236,9 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             if (e + 2 < 16)
               t1 = max3f(t1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
           }
-          // (a group of no page has inv = 0; the scales are positive)
+          // (the scales are positive; a group of no page is left out)
           const float t = fmaxf(t0, t1) * sc[n];
-          mx = fmaxf(mx, inv[n] == 0.0f ? -INFINITY : t);
+          mx = fmaxf(mx, ms[2 * kGroups + n] == 0.0f ? -INFINITY : t);
         }
         float factor = 1.0f;
         if (mx > m_run + kLazyLog2) {
@@ -267,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           uint32_t pk[16];
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float scn = sc[2 * c + n], off = lv[2 * c + n] + neg_m;
+            const float scn = sc[2 * c + n], off = ms[kGroups + 2 * c + n] + neg_m;
             const float2 sc2 = make_float2(scn, scn), of2 = make_float2(off, off);
             const float2 one2 = make_float2(1.0f, 1.0f);
             float2 sum = make_float2(0.0f, 0.0f);
@@ -280,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
               sum = __ffma2_rn(p, one2, sum);
               pk[8 * n + e] = kv8::bf16x2(p.x, p.y);
             }
-            l_run = fmaf(sum.x + sum.y, inv[2 * c + n], l_run);
+            l_run = fmaf(sum.x + sum.y, ms[2 * kGroups + 2 * c + n], l_run);
           }
           tmem_st16(s_addr + 16 * c, pk);
           if (c & 1) {
@@ -324,77 +352,55 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     constexpr int kPer = kDecWarps * 32 / kUnits;   // tokens of a pass
     constexpr int kMine = kKeys / kPer;             // units of a thread and plane
     const uint32_t t = threadIdx.x - kSoftWarps * 32, u = t % kUnits;
+    // threads 0..7: the page scales of a tile's groups, read one tile ahead
     const int32_t* table = a.table + int64_t(b) * a.table_stride;
-    auto token = [&](int j, int i) {
-      return t_begin + j * kKeys + int(t / kUnits) + kPer * i;
+    auto group_page = [&](int j) {
+      const int tok = t_begin + j * kKeys + 16 * int(t);
+      return t < kGroups && tok < t_end ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : -1;
     };
-    auto page_at = [&](int tok) {
-      return tok < t_end ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : -1;
+    float ks = 0.0f, vs = -1.0f;   // vs < 0: no page
+    auto load_scales = [&](int j, int id) {
+      vs = -1.0f;
+      if (id >= 0 && id < a.n_pages) {
+        const int64_t ph = int64_t(id) * a.kv_heads + h;
+        ks = __ldg(a.k_scale + ph);
+        vs = __ldg(a.v_scale + ph);
+      } else if (t < kGroups && t_begin + j * kKeys + 16 * int(t) < t_end) {
+        record_status(a.status, NVFP4_ERR_INVALID_ARG);
+      }
     };
-    auto valid = [&](int tok, int id) { return tok < t_end && id >= 0 && id < a.n_pages; };
-    int pages[kMine], meta_page = -1;
-    uint4 raw[2][kMine];
-    float ks = 0.0f, vs = 0.0f;
-    const int group = int(t);   // threads 0..7: the page scales of a tile's groups
-    auto load_pages = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) pages[i] = page_at(token(j, i));
-      if (group < kGroups) meta_page = page_at(t_begin + j * kKeys + 16 * group);
-    };
-    auto load_codes = [&](int j) {
+    // one plane of a tile: codes of raw stage rs -> operand stage st
+    auto decode = [&](uint32_t raw, uint32_t op) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int tok = token(j, i);
-        raw[0][i] = raw[1][i] = make_uint4(0, 0, 0, 0);
-        if (valid(tok, pages[i])) {
-          const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
-          const int64_t at =
-              ((int64_t(pages[i]) * a.kv_heads + h) * a.page_tokens + in_page) * kD + 16 * u;
-          raw[0][i] = ld_nc_v4(a.k_codes + at);
-          raw[1][i] = ld_nc_v4(a.v_codes + at);
-        }
+        uint4 w;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                     : "r"(raw + (t + kDecWarps * 32 * i) * 16));
+        const uint32_t tok = t / kUnits + kPer * i;
+        const uint2 w0 = decode4(w.x), w1 = decode4(w.y), w2 = decode4(w.z), w3 = decode4(w.w);
+        const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y);
+        const uint4 hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+        // the upper half of the units starts with its second part: other banks
+        const bool swap = u >= 4;
+        st_shared_v4(op + op_offset(tok, 2 * u + swap), swap ? hi : lo);
+        st_shared_v4(op + op_offset(tok, 2 * u + !swap), swap ? lo : hi);
       }
-      if (group < kGroups) {
-        const int tok = t_begin + j * kKeys + 16 * group;
-        ks = vs = 0.0f;
-        if (valid(tok, meta_page)) {
-          const int64_t ph = int64_t(meta_page) * a.kv_heads + h;
-          ks = __ldg(a.k_scale + ph);
-          vs = __ldg(a.v_scale + ph);
-        } else {
-          if (tok < t_end) record_status(a.status, NVFP4_ERR_INVALID_ARG);
-          vs = -1.0f;   // left out
-        }
-      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
     };
+    int next_page = -1;
     if (n_tiles > 0) {
-      load_pages(0);
-      load_codes(0);
-      load_pages(1);
+      load_scales(0, group_page(0));
+      next_page = group_page(1);
     }
     for (int j = 0; j < n_tiles; ++j) {
-      const uint32_t st = j % kStages;
-      if (!__all_sync(0xFFFFFFFFu,
-                      waiter.wait(bar_kv_empty + 8 * st, ((j / kStages) & 1) ^ 1)))
-        break;
-#pragma unroll
-      for (int pl = 0; pl < 2; ++pl) {
-        const uint32_t op = sbase + (pl == 0 ? L::kK : L::kV) + st * L::kOp;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const uint32_t tok = t / kUnits + kPer * i;
-          const uint4 w = raw[pl][i];
-          const uint2 w0 = decode4(w.x), w1 = decode4(w.y), w2 = decode4(w.z), w3 = decode4(w.w);
-          const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y);
-          const uint4 hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
-          // the upper half of the units starts with its second part: other banks
-          const bool swap = u >= 4;
-          st_shared_v4(op + op_offset(tok, 2 * u + swap), swap ? hi : lo);
-          st_shared_v4(op + op_offset(tok, 2 * u + !swap), swap ? lo : hi);
-        }
-      }
-      if (group < kGroups) {
-        float* m = meta + st * 3 * kGroups + group;
+      const uint32_t st = j % kStages, empty = ((j / kStages) & 1) ^ 1;
+      const uint32_t rs = j % L::kRaw, full = (j / L::kRaw) & 1;
+      bool ok = waiter.wait(bar_k_empty + 8 * st, empty) && waiter.wait(bar_rk_full + 8 * rs, full);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (t < kGroups) {
+        float* m = meta + (j % kMetaStages) * kMetaFloats + t;
         const bool none = vs < 0.0f;
         const float v = fmaxf(vs, 0x1p-60f);   // the smallest scale there is
         const uint32_t bits = __float_as_uint(v);
@@ -404,67 +410,102 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                                 __log2f(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
         m[2 * kGroups] = none ? 0.0f : 1.0f / v;
       }
-      if (j + 1 < n_tiles) {
-        load_codes(j + 1);
-        load_pages(j + 2);
+      if (warp == kSoftWarps) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar_meta + 8 * (j % kMetaStages));
+        if (j + 1 < n_tiles) {
+          load_scales(j + 1, next_page);
+          next_page = group_page(j + 2);
+        }
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) bar_arrive(bar_kv_full + 8 * st);
+      decode(sbase + L::kRawK + rs * L::kRawBytes, sbase + L::kK + st * L::kOp);
+      if (lane == 0) {
+        bar_arrive(bar_rk_empty + 8 * rs);
+        bar_arrive(bar_k_full + 8 * st);
+      }
+      ok = waiter.wait(bar_v_empty + 8 * st, empty) && waiter.wait(bar_rv_full + 8 * rs, full);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      decode(sbase + L::kRawV + rs * L::kRawBytes, sbase + L::kV + st * L::kOp);
+      if (lane == 0) {
+        bar_arrive(bar_rv_empty + 8 * rs);
+        bar_arrive(bar_v_full + 8 * st);
+      }
     }
   } else {
     // ------------------------------------------------------------ MMA issuer
     fewer_regs<kMmaRegs>();
-    if (warp == kMmaWarp && lane == 0 && n_tiles > 0) {
-      bool ok = true;
-      for (int g = 0; g < n_q && ok; ++g) ok = waiter.wait(bar_q + 8 * g, 0);
-      // S_g(j) = Q_g K_j^T
-      auto issue_s = [&](uint32_t g, int j) {
-        const uint64_t qd = desc_sw128(sbase + L::kQ + g * L::kOp);
-        const uint64_t kd = desc_sw128(sbase + L::kK + (j % kStages) * L::kOp);
-#pragma unroll
-        for (uint32_t k = 0; k < kD / 16; ++k) {  // 16 dims a step: +32 bytes, next chunk after 4
-          const uint32_t at = (k >> 2) * (kChunkBytes >> 4) + 2 * (k & 3);
-          mma_ss(tmem + kSCol0 + 128 * g, qd + at, kd + at, idesc(kKeys), k != 0);
-        }
-        tc_commit(bar_s_full + 8 * g);
+    if (warp == kMmaWarp && n_tiles > 0) {
+      // the whole warp, so that operands are uniform; one lane issues
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, waiter.wait(bar, parity));
       };
-      // O_g += P_g(j) V_j, as the halves of P come
+      bool ok = true;
+      for (int g = 0; g < n_q && ok; ++g) ok = wait(bar_q + 8 * g, 0);
+      // low descriptor words: K-major with LBO 1, MN-major with the chunk stride
+      const uint32_t lo_k = ((sbase & 0x3FFFFu) >> 4) | (1u << 16);
+      const uint32_t lo_mn = ((sbase & 0x3FFFFu) >> 4) | (uint32_t(kChunkBytes >> 4) << 16);
+      // S_g(j) = Q_g K_j^T: 16 dims a step, +32 bytes, the next chunk after 4
+      auto issue_s = [&](uint32_t g, int j) {
+        const uint32_t qd = lo_k + ((L::kQ + g * L::kOp) >> 4);
+        const uint32_t kd = lo_k + ((L::kK + (j % kStages) * L::kOp) >> 4);
+        unrolled(
+            [&](auto k) {
+              constexpr uint32_t at = (k.value >> 2) * (kChunkBytes >> 4) + 2 * (k.value & 3);
+              warp_mma_ss<at, at>(tmem + kSCol0 + 128 * g, qd, kd, idesc(kKeys), k.value != 0);
+            },
+            std::make_integer_sequence<uint32_t, kD / 16>());
+        warp_commit(bar_s_full + 8 * g);
+      };
+      // O_g += P_g(j) V_j, as the halves of P come: 16 keys a step, 8 columns of P
       auto issue_pv = [&](uint32_t g, int j) {
-        const uint64_t vd = desc_mn_sw128(sbase + L::kV + (j % kStages) * L::kOp);
-#pragma unroll
-        for (uint32_t half = 0; half < 2; ++half) {
-          if (!waiter.wait(bar_p_ready + 16 * g + 8 * half, j & 1)) return false;
-          tc_fence_after();
-#pragma unroll
-          for (uint32_t k = 4 * half; k < 4 * half + 4; ++k)  // 16 keys: 8 columns of P
-            mma_ts(tmem + kOCol0 + 128 * g, tmem + kSCol0 + 128 * g + 8 * k, vd + k * (2048 >> 4),
-                   idesc(kD) | (1u << 16), (j | k) != 0);
-        }
-        tc_commit(bar_pv_done + 8 * g);
+        const uint32_t vd = lo_mn + ((L::kV + (j % kStages) * L::kOp) >> 4);
+        const uint32_t od = tmem + kOCol0 + 128 * g, pd = tmem + kSCol0 + 128 * g;
+        if (!wait(bar_p_ready + 16 * g, j & 1)) return false;
+        tc_fence_after();
+        unrolled(
+            [&](auto k) {
+              warp_mma_ts<8 * k.value, k.value * (2048 >> 4)>(od, pd, vd, idesc(kD) | (1u << 16),
+                                                              k.value != 0 || j != 0);
+            },
+            std::make_integer_sequence<uint32_t, 4>());
+        if (!wait(bar_p_ready + 16 * g + 8, j & 1)) return false;
+        tc_fence_after();
+        unrolled(
+            [&](auto k) {
+              warp_mma_ts<32 + 8 * k.value, (4 + k.value) * (2048 >> 4)>(
+                  od, pd, vd, idesc(kD) | (1u << 16), 1);
+            },
+            std::make_integer_sequence<uint32_t, 4>());
+        warp_commit(bar_pv_done + 8 * g);
         return true;
       };
-      auto kv_ready = [&](int j) {
-        if (!waiter.wait(bar_kv_full + 8 * (j % kStages), (j / kStages) & 1)) return false;
+      auto ready = [&](uint32_t bar, int j) {
+        if (!wait(bar + 8 * (j % kStages), (j / kStages) & 1)) return false;
         tc_fence_after();
         return true;
       };
-      if (ok && (ok = kv_ready(0)))
+      if (ok && (ok = ready(bar_k_full, 0))) {
         for (int g = 0; g < n_q; ++g) issue_s(g, 0);
+        warp_commit(bar_k_empty);
+      }
       for (int j = 0; j < n_tiles && ok; ++j) {
         const bool more = j + 1 < n_tiles;
-        for (int g = 0; g < n_q && ok; ++g) {
+#pragma unroll 1
+        for (int g = 0; g < n_q; ++g) {
+          const bool last = g == n_q - 1;
+          if (g == 0 && !(ok = ready(bar_v_full, j))) break;
           if (!(ok = issue_pv(g, j))) break;
-          if (g == n_q - 1) tc_commit(bar_kv_empty + 8 * (j % kStages));  // stage j read
+          if (last) warp_commit(bar_v_empty + 8 * (j % kStages));
           if (more) {
-            if (g == 0 && !(ok = kv_ready(j + 1))) break;
+            if (g == 0 && !(ok = ready(bar_k_full, j + 1))) break;
             issue_s(g, j + 1);
+            if (last) warp_commit(bar_k_empty + 8 * ((j + 1) % kStages));
           }
         }
       }
-      if (ok) tc_commit(bar_o_full);
-      // drain: every tcgen05 operation this thread issued has completed
-      tc_commit(bar_drain);
+      if (ok) warp_commit(bar_o_full);
+      // drain: every tcgen05 operation this warp issued has completed
+      warp_commit(bar_drain);
       const uint64_t t0 = globaltimer();
       while (!bar_try_wait(bar_drain, 0)) {
         if (globaltimer() - t0 > 2000000000ull) {
@@ -472,6 +513,59 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           break;
         }
       }
+    } else if (warp == kLoadWarp) {
+      // ---------------------------------------------------------- codes, a tile ahead
+      const int32_t* table = a.table + int64_t(b) * a.table_stride;
+      auto page_of = [&](int j) {   // lanes 0..7: the groups' pages, -1 for none
+        const int tok = t_begin + j * kKeys + 16 * lane;
+        const int id = lane < kGroups && tok < t_end
+                           ? __ldg(table + fast_div(a.page_div, uint32_t(tok)))
+                           : -1;
+        return id < a.n_pages ? id : -1;
+      };
+      constexpr uint32_t kBytes = 16 * kD;   // of a group
+      int page = page_of(0), j = 0;
+      for (; j < n_tiles; ++j) {
+        const int next = page_of(j + 1);
+        const uint32_t rs = j % L::kRaw, empty = ((j / L::kRaw) & 1) ^ 1;
+        const int tok = t_begin + j * kKeys + 16 * lane;
+        const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
+        const int64_t at = ((int64_t(max(page, 0)) * a.kv_heads + h) * a.page_tokens + in_page) * kD;
+        const uint32_t live = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0));
+        bool ok = true;
+#pragma unroll
+        for (int pl = 0; pl < 2 && ok; ++pl) {
+          const uint32_t full = (pl ? bar_rv_full : bar_rk_full) + 8 * rs;
+          ok = __all_sync(0xFFFFFFFFu,
+                          waiter.wait((pl ? bar_rv_empty : bar_rk_empty) + 8 * rs, empty));
+          if (!ok) break;
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
+                         "r"(live * kBytes)
+                         : "memory");
+          __syncwarp();
+          if (page >= 0)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], "
+                "%2, [%3];" ::"r"(sbase + (pl ? L::kRawV : L::kRawK) + rs * L::kRawBytes +
+                                  lane * kBytes),
+                "l"((pl ? a.v_codes : a.k_codes) + at), "r"(kBytes), "r"(full)
+                : "memory");
+          __syncwarp();
+        }
+        if (!ok) break;
+        page = next;
+      }
+      // drain: every copy issued has landed before the CTA may leave (an abort may have come
+      // between a tile's K and V: its K is waited for, its V was not begun)
+      for (int pl = 0; pl < 2; ++pl)
+        for (int d = max(0, j - L::kRaw); d < (pl == 0 ? min(j + 1, n_tiles) : j); ++d) {
+          const uint32_t full = (pl ? bar_rv_full : bar_rk_full) + 8 * (d % L::kRaw);
+          const uint64_t t0 = globaltimer();
+          while (!bar_try_wait(full, (d / L::kRaw) & 1)) {
+            if (globaltimer() - t0 > 2000000000ull) break;
+          }
+        }
     }
     __syncwarp();
   }

@@ -1,6 +1,8 @@
 // tc.cuh -- what the attention kernels share of the sm_100a tensor core: barriers, tensor
 // memory, bf16 tcgen05.mma on 128-byte-swizzled operands, bounded waits.
 #pragma once
+#include <utility>
+
 #include "common.cuh"
 
 namespace nvfp4 {
@@ -76,6 +78,47 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// The same for a whole converged warp, one lane of which issues: the operands stay in uniform
+// registers, which saves the moves there that a lone thread makes for every instruction.
+// Descriptors come as their low words (kDescHi is the high one) and a constant to add.
+constexpr uint32_t kDescHi = uint32_t(1024 >> 4) | (1u << 14) | (2u << 29);
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void warp_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 x, y;\n\t.reg .b64 da, db;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 x, %1, %5;\n\t"
+      "add.u32 y, %2, %6;\n\t"
+      "mov.b64 da, {x, %7};\n\t"
+      "mov.b64 db, {y, %7};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kA), "n"(kB), "r"(kDescHi)
+      : "memory");
+}
+template <uint32_t kA, uint32_t kB>
+__device__ __forceinline__ void warp_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b32 x, y;\n\t.reg .b64 db;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "add.u32 x, %1, %5;\n\t"
+      "add.u32 y, %2, %6;\n\t"
+      "mov.b64 db, {y, %7};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "n"(kA), "n"(kB), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          bar)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -171,6 +214,12 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
 }
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// f(integral_constant<0>) .. f(integral_constant<kN - 1>)
+template <typename F, uint32_t... kI>
+__device__ __forceinline__ void unrolled(F&& f, std::integer_sequence<uint32_t, kI...>) {
+  (f(std::integral_constant<uint32_t, kI>()), ...);
 }
 
 // Byte offset of 16-byte unit u (0..15: elements 8u..8u+7) of row r in a
