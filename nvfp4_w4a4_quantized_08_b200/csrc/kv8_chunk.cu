@@ -4,31 +4,41 @@
 //   out[t][h] = sum_j softmax_j(scale q[t][h] . k[j]) v[j],  k = codes * page scale
 //
 // Bound by the softmax (one exponential for each row and token: 16 a clock and SM) and the
-// tensor core (bf16 S = Q K^T and P V), which take about the same time per tile of 128 x
+// tensor core (fp16 S = Q K^T and P V), which take about the same time per tile of 128 x
 // 128; so both have to run all the time.  One CTA of 16 warps takes 256 packed rows (two
 // tiles of 128) of one request and KV head and a range of its tokens:
 //   warps 0..7   softmax: warpgroup g owns row tile g, one row a thread.  A row's 128
 //                scores of a tile are read from tensor memory once, into registers
 //                (200 a thread, moved over from the other warps by setmaxnreg); the
-//                probabilities go back as bf16, in two halves, so that P V starts on the
-//                first while the second is computed.
-//   warps 8..11  decoders: E4M3 codes -> bf16 K and V operands in 128-byte-swizzled shared
-//                memory (two stages each).  A code is shifted into place and multiplied by
-//                2^120, two at a time: exact.  The order of 8 dims is the one in which that
-//                needs no byte permutes (0 2 1 3 4 6 5 7); Q is stored in the same order, the
-//                output is read in it.  Every byte decodes to something finite, so tokens past
-//                the end need no clearing: their probabilities are 0.
-//   warp 12      issues the MMAs: ... PV0_j, S0_{j+1}, PV1_j, S1_{j+1}, PV0_{j+1} ..., so
-//                the tensor core works on one row tile while the other's softmax runs.
+//                probabilities go back as fp16.
+//   warps 8..11  decoders: E4M3 codes -> fp16 K and V operands in 128-byte-swizzled shared
+//                memory (two stages each), one hardware conversion per two codes, exact.
+//                (bf16 operands took 4.5 times the instructions, and set the pace.)
+//   warp 12, 14  issue the MMAs, one S and one P V.
 //   warp 13      copies the codes of a tile ahead (one bulk copy for the 16 tokens of a group,
 //                which share a page).
-// Tensor memory (512 columns): O0, O1, S0, S1; P_g takes S_g's place.
+// Tensor memory (512 columns): O0, O1, one S, P0, P1.  Both row tiles use the one S in turn:
+// it is free again as soon as a softmax has read it, so the next S is there before the
+// softmax that needs it is done with the last one, and no S waits for a P V.
 //
-// The codes go into the products without their page scales.  Scores of a group of 16 tokens
-// are multiplied by the page's K scale in fp32; its V scale is an exponent added to the
-// probabilities' (P is bf16, which holds it), and the normaliser takes the group's sum times
-// 2^-exponent: exact, and one multiplication a group.  The running maximum is raised lazily:
-// only a step of more than 2^16 rescales O and the sum.
+// What a softmax warp executes sets the pace: two of them a scheduler, each alone with its
+// latencies.  So it looks for no maximum: the weights of a tile are taken against the
+// reference in use, and only where a sum of 16 of them shows that one might be too large for
+// fp16 is the tile taken again, in a slower form that finds the maximum and raises the
+// reference.  2640 rows over 10560 tokens and 24 heads: 429 us with the maximum taken every
+// time, 375 without (913 TFLOP/s, 55% of the measured bf16 burst; 269 with no exponentials
+// and no decoding at all).  On the way there: 624 us with S and P in one place and one MMA
+// warp; 456 with rings of their own for K and V; what did not help: sixteen softmax warps
+// of half a row each (517), a quarter of the exponentials as polynomials on the FMA pipe
+// (478 against 458), and warps that take turns at the exponentials (493 against 458).
+//
+// The codes go into the products without their page scales.  Q is scaled by a power of two
+// per row to fp16 (largest element in [2^8, 2^9): exact for elements within 2^-22 of it, an
+// error of at most 2^-33 of it below).  Scores of a group of 16 tokens are multiplied by the
+// page's K scale in fp32.  The page's V scale is an exponent added to the probability's:
+// these weights 2^(x + log2 s_v) go into P relative to the reference, which follows their
+// maximum (2^9 there; an error of at most 2^-34 of it where they become subnormal), and the
+// normaliser takes a group's sum times 2^-exponent: exact, and one multiplication a group.
 //
 // Every wait is bounded: one that runs out records NVFP4_ERR_TIMEOUT in the status word, and
 // the CTA drains its MMAs, frees tensor memory and returns.
@@ -52,17 +62,20 @@ constexpr int kSoftWarps = 8;              // warps 0..7
 constexpr int kDecWarps = 4;               // warps 8..11
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
 constexpr int kThreads = 512;              // four warpgroups; the last has the MMA warp only
-constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kLoadWarp = kMmaWarp + 1, kPvWarp = kMmaWarp + 2;
 constexpr int kStages = 2;                 // decoded tiles of K, and of V
 constexpr int kMetaStages = 4;             // page scales: read later than K
-constexpr int kMetaFloats = 3 * kGroups;
+constexpr int kMetaFloats = 3 * kGroups + 1;   // and whether the tile is wide
 // registers a thread at launch, and after the warpgroups have shared them out anew
 constexpr int kLaunchRegs = 128, kSoftRegs = 200, kDecRegs = 56, kMmaRegs = 56;
 static_assert(2 * kSoftRegs + kDecRegs + kMmaRegs == 4 * kLaunchRegs, "register split");
 static_assert(kThreads * kLaunchRegs <= 65536, "registers of an SM");
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kOCol0 = 0, kSCol0 = 256;   // O_g at 128 g, S_g (then P_g) at 256 + 128 g
-constexpr float kLazyLog2 = 16.0f;
+// tensor memory columns: O_g at 128 g, S, P_g (fp16 pairs) at kPCol0 + 64 g
+constexpr uint32_t kOCol0 = 0, kSCol0 = 256, kPCol0 = 384;
+constexpr float kBias = 9.0f;     // the largest weight is 2^9 when it sets the reference,
+constexpr float kLazy = 2.0f;     // and sets it where it would be more than 2^11
+constexpr float kWide = 28.0f;    // |log2 s_v| above which a tile takes the slower exponentials
 
 template <int kD>
 struct Layout {
@@ -72,32 +85,38 @@ struct Layout {
   static constexpr int kRaw = kD == 64 ? 3 : 1;            // tiles of codes ahead
   static constexpr int kRawBytes = kKeys * kD;             // of one plane
   static constexpr int kRawK = kV + kStages * kOp, kRawV = kRawK + kRaw * kRawBytes;
-  static constexpr int kMeta = kRawV + kRaw * kRawBytes;   // [stage][3][group] floats
-  static constexpr int kBar = kMeta + kMetaStages * kMetaFloats * 4;
-  // q[2], k_full, k_empty, v_full, v_empty [stage], s_full[2], p_ready[2][2], pv_done[2],
-  // meta_full[4], raw K full, empty, raw V full, empty [raw stage], o_full, drain
-  static constexpr int kNumBars = 2 + 4 * kStages + 2 + 4 + 2 + kMetaStages + 4 * kRaw + 2;
+  static constexpr int kMeta = kRawV + kRaw * kRawBytes;
+  static constexpr int kBar = (kMeta + kMetaStages * kMetaFloats * 4 + 7) / 8 * 8;
+  // q[2], k_full, k_empty, v_full, v_empty [stage], s_full[2], s_free, p_ready[2],
+  // pv_done[2], meta_full[4], raw K full, empty, raw V full, empty [raw stage], o_full, drain[2]
+  static constexpr int kNumBars = 2 + 4 * kStages + 2 + 1 + 2 + 2 + kMetaStages + 4 * kRaw + 3;
   static constexpr int kTmemPtr = kBar + kNumBars * 8;
   static constexpr int kAbort = kTmemPtr + 4;
   static constexpr int kBytes = kAbort + 4 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
 
-// kind::f16: fp32 D (bit 4), bf16 A and B (bits 7 and 10), N >> 3 at 17, M >> 4 at 24; B
-// MN-major: bit 16.
+// kind::f16: fp32 D (bit 4), fp16 A and B, N >> 3 at 17, M >> 4 at 24; B MN-major: bit 16.
 __host__ __device__ constexpr uint32_t idesc(uint32_t n) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
+  return (1u << 4) | ((n >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
 }
 
-// Four E4M3 bytes -> bf16 of bytes (0, 2) and (1, 3): sign and the 7 other bits into place,
-// which is the value times 2^-120 (subnormals too), then times 2^120.
+// Four E4M3 bytes -> two fp16 pairs, exact.
 __device__ __forceinline__ uint2 decode4(uint32_t w) {
-  uint32_t lo = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
-  uint32_t hi = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
-  const uint32_t k120 = 0x7B807B80u;
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(k120));
-  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(hi) : "r"(k120));
-  return make_uint2(lo, hi);
+  uint2 r;
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 template <int kRegs>
@@ -131,8 +150,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const uint32_t bar_v_full = bar_k_empty + 8 * kStages;
   const uint32_t bar_v_empty = bar_v_full + 8 * kStages;
   const uint32_t bar_s_full = bar_v_empty + 8 * kStages;       // + 8 g
-  const uint32_t bar_p_ready = bar_s_full + 8 * kTiles;        // + 16 g + 8 half
-  const uint32_t bar_pv_done = bar_p_ready + 16 * kTiles;      // + 8 g
+  const uint32_t bar_s_free = bar_s_full + 8 * kTiles;
+  const uint32_t bar_p_ready = bar_s_free + 8;                 // + 8 g
+  const uint32_t bar_pv_done = bar_p_ready + 8 * kTiles;       // + 8 g
   const uint32_t bar_meta = bar_pv_done + 8 * kTiles;          // + 8 stage
   const uint32_t bar_rk_full = bar_meta + 8 * kMetaStages;     // + 8 raw stage
   const uint32_t bar_rk_empty = bar_rk_full + 8 * L::kRaw;
@@ -153,8 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     for (int g = 0; g < kTiles; ++g) {
       bar_init(bar_q + 8 * g, 4);
       bar_init(bar_s_full + 8 * g, 1);
-      bar_init(bar_p_ready + 16 * g, 4);
-      bar_init(bar_p_ready + 16 * g + 8, 4);
+      bar_init(bar_p_ready + 8 * g, 4);
       bar_init(bar_pv_done + 8 * g, 1);
     }
     for (int s = 0; s < kStages; ++s) {
@@ -170,8 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       bar_init(bar_rv_full + 8 * s, 1);
       bar_init(bar_rv_empty + 8 * s, kDecWarps);
     }
+    bar_init(bar_s_free, 4);
     bar_init(bar_o_full, 1);
     bar_init(bar_drain, 1);
+    bar_init(bar_drain + 8, 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -188,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const uint32_t tmem = *tmem_ptr;
   pdl_wait();
   pdl_trigger();
-  const Waiter waiter{a.wait_limit_ns, abort_flag, a.status};
+  const WarpWaiter waiter{{a.wait_limit_ns, abort_flag, a.status}};
 
   const Request rq = kv8::request(a, b, threadIdx.x == 0 && blockIdx.x == 0 && split == 0);
   const int rows = rq.nq * a.group, base = tile * kRows * kTiles;
@@ -206,126 +227,183 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     more_regs<kSoftRegs>();
     const uint32_t g = uint32_t(warp) >> 2, quad = uint32_t(warp) & 3;
     const uint32_t row = quad * 32 + uint32_t(lane);
-    const uint32_t o_addr = tmem + ((quad * 32) << 16) + kOCol0 + 128 * g;
-    const uint32_t s_addr = tmem + ((quad * 32) << 16) + kSCol0 + 128 * g;
+    const uint32_t lanes = tmem + ((quad * 32) << 16);
+    const uint32_t o_addr = lanes + kOCol0 + 128 * g, p_addr = lanes + kPCol0 + 64 * g;
+    const uint32_t s_addr = lanes + kSCol0;
     const int rho = base + int(g) * kRows + int(row);
     const bool live = int(g) < n_q && rho < rows;
     // tokens of the range that this row sees (dead rows follow the last live one)
     const int vis = min(t_range, kv8::sees(a, rq, max(0, min(rho, rows - 1)))) - t_begin;
     const int vis_min = __reduce_min_sync(0xFFFFFFFFu, vis);
     bool ok = true;
-    float m_run = -INFINITY, l_run = 0.0f;
+    // l and O are in units of 2^ref, ref the largest weight's logarithm less kBias (about: see
+    // below); seen: a token has set it
+    float ref = 0.0f, l_run = 0.0f;
+    bool seen = false, all_seen = false;
     if (int(g) < n_q && n_tiles > 0) {
-      // Q row -> shared memory in the dims' order of the decoders
+      // Q row -> fp16 in shared memory, its power of two into the scores' scale
       const uint4* src =
           reinterpret_cast<const uint4*>(live ? kv8::q_row(a, rq, h, rho, kD) : a.q);
-      const uint32_t qs = sbase + L::kQ + g * L::kOp;
+      uint32_t top = 0;
 #pragma unroll 4
       for (uint32_t u = 0; u < kD / 8; ++u) {
-        uint4 v = live ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
-        v = make_uint4(prmt(v.x, v.y, 0x5410), prmt(v.x, v.y, 0x7632), prmt(v.z, v.w, 0x5410),
-                       prmt(v.z, v.w, 0x7632));
-        st_shared_v4(qs + op_offset(row, u), v);
+        const uint4 v = live ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                                     __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+      }
+      const uint32_t field = min(262u - (max(top & 0xFFFFu, top >> 16) >> 7), 253u);
+      const float up = __uint_as_float(field << 23);
+      const float q_scale = __uint_as_float((254u - field) << 23);
+      const uint32_t qs = sbase + L::kQ + g * L::kOp;
+      auto half2 = [&](uint32_t w) {
+        return f16x2_rn(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+      };
+#pragma unroll 4
+      for (uint32_t u = 0; u < kD / 8; ++u) {
+        const uint4 v = live ? __ldg(src + u) : make_uint4(0, 0, 0, 0);
+        st_shared_v4(qs + op_offset(row, u),
+                     make_uint4(half2(v.x), half2(v.y), half2(v.z), half2(v.w)));
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) bar_arrive(bar_q + 8 * g);
       for (int j = 0; j < n_tiles; ++j) {
-        ok = __all_sync(0xFFFFFFFFu, waiter.wait(bar_meta + 8 * (j % kMetaStages),
-                                                 (j / kMetaStages) & 1));
+        ok = waiter.wait(bar_meta + 8 * (j % kMetaStages),
+                                                 (j / kMetaStages) & 1);
         if (!ok) break;
         // per group: K scale times scale * log2 e; log2 of the V scale; 1 / V scale (0: no
-        // page, left out)
+        // page, left out, with a log2 of -inf)
         const float* ms = meta + (j % kMetaStages) * kMetaFloats;
-        float sc[kGroups];
-#pragma unroll
-        for (int n = 0; n < kGroups; ++n) sc[n] = ms[n];
-        ok = __all_sync(0xFFFFFFFFu, waiter.wait(bar_s_full + 8 * g, j & 1));
+        const bool slow = vis_min < (j + 1) * kKeys || ms[3 * kGroups] != 0.0f;
+        ok = waiter.wait(bar_s_full + 8 * g, j & 1);
         if (!ok) break;
         tc_fence_after();
         uint32_t r[4][32];
         load_scores(s_addr, r);
-        if (vis_min < (j + 1) * kKeys) {
-          const int left = vis - j * kKeys;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * c + e >= left) r[c][e] = 0xFF800000u;
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int n = 0; n < kGroups; ++n) {
-          const uint32_t* s = &r[n >> 1][16 * (n & 1)];
-          float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]);
-#pragma unroll
-          for (int e = 2; e < 16; e += 4) {
-            t0 = max3f(t0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-            if (e + 2 < 16)
-              t1 = max3f(t1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
-          }
-          // (the scales are positive; a group of no page is left out)
-          const float t = fmaxf(t0, t1) * sc[n];
-          mx = fmaxf(mx, ms[2 * kGroups + n] == 0.0f ? -INFINITY : t);
-        }
-        float factor = 1.0f;
-        if (mx > m_run + kLazyLog2) {
-          factor = exp2_approx(m_run - mx);   // 0 on the first tokens
-          m_run = mx;
-          l_run *= factor;
-        }
-        if (__any_sync(0xFFFFFFFFu, factor != 1.0f) && j > 0) {
-          // tile j - 1's P V is complete, since S of tile j is
-          ok = __all_sync(0xFFFFFFFFu, waiter.wait(bar_pv_done + 8 * g, (j - 1) & 1));
-          if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar_s_free);
+        if (j > 0) {   // tile j - 1's P V has read P, and written O
+          if (!(ok = waiter.wait(bar_pv_done + 8 * g, (j - 1) & 1))) break;
           tc_fence_after();
-#pragma unroll 1
-          for (uint32_t c = 0; c < kD / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(o_addr + 16 * c, o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
-            tmem_st16(o_addr + 16 * c, o);
-          }
         }
-        const float neg_m = m_run == -INFINITY ? 0.0f : -m_run;
+        // Weights against the reference in use, without looking for a maximum first: a weight
+        // cannot be too large for fp16 where no sum of 16 exceeds 2^15.
+        bool again = slow || !all_seen;
+        if (!again) {
+          float l = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const float scn = sc[2 * c + n], off = ms[kGroups + 2 * c + n] + neg_m;
-            const float2 sc2 = make_float2(scn, scn), of2 = make_float2(off, off);
-            const float2 one2 = make_float2(1.0f, 1.0f);
-            float2 sum = make_float2(0.0f, 0.0f);
+            for (int n = 0; n < 2; ++n) {
+              const float scn = ms[2 * c + n] * q_scale, off = ms[kGroups + 2 * c + n] - ref;
+              const float2 sc2 = make_float2(scn, scn), of2 = make_float2(off, off);
+              const float2 one2 = make_float2(1.0f, 1.0f);
+              float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(r[c][16 * n + 2 * e]),
-                                                      __uint_as_float(r[c][16 * n + 2 * e + 1])),
-                                          sc2, of2);
-              const float2 p = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-              sum = __ffma2_rn(p, one2, sum);
-              pk[8 * n + e] = kv8::bf16x2(p.x, p.y);
+              for (int e = 0; e < 8; ++e) {
+                const float2 x =
+                    __ffma2_rn(make_float2(__uint_as_float(r[c][16 * n + 2 * e]),
+                                           __uint_as_float(r[c][16 * n + 2 * e + 1])),
+                               sc2, of2);
+                const float2 w = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                sum = __ffma2_rn(w, one2, sum);
+                pk[8 * n + e] = f16x2_rn(w.x, w.y);
+              }
+              const float both = sum.x + sum.y;
+              l = fmaf(both, ms[2 * kGroups + 2 * c + n], l);
+              again |= !(both <= 32768.0f);   // (true for NaN)
             }
-            l_run = fmaf(sum.x + sum.y, ms[2 * kGroups + 2 * c + n], l_run);
+            tmem_st16(p_addr + 16 * c, pk);
           }
-          tmem_st16(s_addr + 16 * c, pk);
-          if (c & 1) {
-            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bar_p_ready + 16 * g + 8 * (c >> 1));
+          again = __any_sync(0xFFFFFFFFu, again);
+          if (!again) l_run += l;
+        }
+        if (again) {
+          // The slower form, until every row has seen a token, for masked tiles (exact zeros), V scales far from 1,
+          // and a new maximum: the reference rises to it, l and O are rescaled, and the V scale
+          // is multiplied in after the exponential, so that a token counts for the normaliser
+          // even where its weight is lost against the largest.
+          if (vis_min < (j + 1) * kKeys) {
+            const int left = vis - j * kKeys;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= left) r[c][e] = 0xFF800000u;
+          }
+          float mx = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < kGroups; ++n) {
+            const uint32_t* s = &r[n >> 1][16 * (n & 1)];
+            float t0 = __uint_as_float(s[0]), t1 = __uint_as_float(s[1]);
+#pragma unroll
+            for (int e = 2; e < 16; e += 4) {
+              t0 = max3f(t0, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+              if (e + 2 < 16)
+                t1 = max3f(t1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+            }
+            // (the scales are positive; a group of no page has a log2 of -inf)
+            mx = fmaxf(mx, fmaf(fmaxf(t0, t1), ms[n] * q_scale, ms[kGroups + n]));
+          }
+          float factor = 1.0f;
+          if (mx - kBias > ref + kLazy || !seen) {
+            if (mx > -INFINITY) {
+              factor = seen ? exp2_approx(ref - (mx - kBias)) : 0.0f;
+              ref = mx - kBias;
+              seen = true;
+              l_run *= factor;
+            }
+          }
+          all_seen = __all_sync(0xFFFFFFFFu, seen);
+          if (j > 0 && __any_sync(0xFFFFFFFFu, factor != 1.0f)) {
+#pragma unroll 1
+            for (uint32_t c = 0; c < kD / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(o_addr + 16 * c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+              tmem_st16(o_addr + 16 * c, o);
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float scn = ms[2 * c + n] * q_scale;
+              // a group of no page: 0 for the normaliser too
+              const float lv = ms[kGroups + 2 * c + n];
+              const float none = lv == -INFINITY ? -INFINITY : -ref, sv = exp2f(lv);
+              float sum = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float x0 =
+                    exp2_approx(fmaf(__uint_as_float(r[c][16 * n + 2 * e]), scn, none));
+                const float x1 =
+                    exp2_approx(fmaf(__uint_as_float(r[c][16 * n + 2 * e + 1]), scn, none));
+                sum += x0 + x1;
+                pk[8 * n + e] = f16x2_rn(x0 * sv, x1 * sv);
+              }
+              l_run += sum;
+            }
+            tmem_st16(p_addr + 16 * c, pk);
           }
         }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(bar_p_ready + 8 * g);
       }
-      if (ok) ok = __all_sync(0xFFFFFFFFu, waiter.wait(bar_o_full, 0));
+      if (ok) ok = waiter.wait(bar_o_full, 0);
       tc_fence_after();
     }
     // ---- O / l -> the output or the range's part; a row that saw nothing is zero
     if (ok && int(g) < n_q) {
       const float norm = l_run == 0.0f ? 0.0f : 1.0f / l_run;
-      const float lse2 = l_run == 0.0f ? -INFINITY : m_run + log2f(l_run);
+      const float lse2 = l_run == 0.0f ? -INFINITY : ref + log2f(l_run);
 #pragma unroll 1
       for (uint32_t c = 0; c < kD / 16; ++c) {
         uint32_t o[16];
@@ -338,9 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         float v[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          // dims 1 and 2, 5 and 6 of every 8 change places
-          const int from = (e & 3) == 1 ? e + 1 : (e & 3) == 2 ? e - 1 : e;
-          v[e] = l_run == 0.0f ? 0.0f : __uint_as_float(o[from]) * norm;
+          v[e] = l_run == 0.0f ? 0.0f : __uint_as_float(o[e]) * norm;
         }
         if (live) kv8::store_row<16, kD>(a, rq, h, rho, split, used, 16 * c, v, lse2, c == 0);
       }
@@ -369,26 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         record_status(a.status, NVFP4_ERR_INVALID_ARG);
       }
     };
-    // one plane of a tile: codes of raw stage rs -> operand stage st
-    auto decode = [&](uint32_t raw, uint32_t op) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        uint4 w;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                     : "r"(raw + (t + kDecWarps * 32 * i) * 16));
-        const uint32_t tok = t / kUnits + kPer * i;
-        const uint2 w0 = decode4(w.x), w1 = decode4(w.y), w2 = decode4(w.z), w3 = decode4(w.w);
-        const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y);
-        const uint4 hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
-        // the upper half of the units starts with its second part: other banks
-        const bool swap = u >= 4;
-        st_shared_v4(op + op_offset(tok, 2 * u + swap), swap ? hi : lo);
-        st_shared_v4(op + op_offset(tok, 2 * u + !swap), swap ? lo : hi);
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-    };
     int next_page = -1;
     if (n_tiles > 0) {
       load_scales(0, group_page(0));
@@ -397,20 +453,21 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
     for (int j = 0; j < n_tiles; ++j) {
       const uint32_t st = j % kStages, empty = ((j / kStages) & 1) ^ 1;
       const uint32_t rs = j % L::kRaw, full = (j / L::kRaw) & 1;
-      bool ok = waiter.wait(bar_k_empty + 8 * st, empty) && waiter.wait(bar_rk_full + 8 * rs, full);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      if (t < kGroups) {
+      const int left = t_end - t_begin - j * kKeys;
+      if (warp == kSoftWarps) {
         float* m = meta + (j % kMetaStages) * kMetaFloats + t;
         const bool none = vs < 0.0f;
         const float v = fmaxf(vs, 0x1p-60f);   // the smallest scale there is
         const uint32_t bits = __float_as_uint(v);
-        m[0] = none ? 1.0f : ks * a.scale_log2;   // (not 0: a masked score is -inf)
-        m[kGroups] = none ? -INFINITY
-                          : float(int(bits >> 23) - 127) +
-                                __log2f(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
-        m[2 * kGroups] = none ? 0.0f : 1.0f / v;
-      }
-      if (warp == kSoftWarps) {
+        const float lv = float(int(bits >> 23) - 127) +
+                         __log2f(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
+        if (t < kGroups) {
+          m[0] = none ? 1.0f : ks * a.scale_log2;   // (not 0: a masked score is -inf)
+          m[kGroups] = none ? -INFINITY : lv;
+          m[2 * kGroups] = none ? 0.0f : 1.0f / v;
+        }
+        const bool wide = __any_sync(0xFFFFFFFFu, t < kGroups && !none && fabsf(lv) > kWide);
+        if (t == 0) m[3 * kGroups] = wide ? 1.0f : 0.0f;
         __syncwarp();
         if (lane == 0) bar_arrive(bar_meta + 8 * (j % kMetaStages));
         if (j + 1 < n_tiles) {
@@ -418,96 +475,116 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           next_page = group_page(j + 2);
         }
       }
-      decode(sbase + L::kRawK + rs * L::kRawBytes, sbase + L::kK + st * L::kOp);
-      if (lane == 0) {
-        bar_arrive(bar_rk_empty + 8 * rs);
-        bar_arrive(bar_k_full + 8 * st);
+      // K, then V: codes of raw stage rs -> operand stage st.  (Rolled loops: the softmax code
+      // alone fills the instruction cache; unrolled decoders cost a quarter of the rate.)
+      bool ok = true;
+#pragma unroll 1
+      for (int pl = 0; pl < 2; ++pl) {
+        const uint32_t bar_empty = (pl ? bar_v_empty : bar_k_empty) + 8 * st;
+        const uint32_t bar_full = (pl ? bar_v_full : bar_k_full) + 8 * st;
+        const uint32_t bar_raw = (pl ? bar_rv_full : bar_rk_full) + 8 * rs;
+        const uint32_t bar_raw_empty = (pl ? bar_rv_empty : bar_rk_empty) + 8 * rs;
+        ok = waiter.wait(bar_empty, empty) && waiter.wait(bar_raw, full);
+                if (!ok) break;
+        const uint32_t raw = sbase + (pl ? L::kRawV : L::kRawK) + rs * L::kRawBytes + t * 16;
+        const uint32_t op = sbase + (pl ? L::kV : L::kK) + st * L::kOp;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kMine; i0 += 4) {   // four loads in flight
+          uint4 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                         : "r"(raw + kDecWarps * 32 * 16 * (i0 + i)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t tok = t / kUnits + kPer * (i0 + i);
+            // past the range's end there may be anything, NaN codes included: 0
+            if (int(tok) >= left) w[i] = make_uint4(0, 0, 0, 0);
+            const uint2 w0 = decode4(w[i].x), w1 = decode4(w[i].y);
+            const uint2 w2 = decode4(w[i].z), w3 = decode4(w[i].w);
+            const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y);
+            const uint4 hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+            // the upper half of the units starts with its second part: other banks
+            const bool swap = u >= 4;
+            st_shared_v4(op + op_offset(tok, 2 * u + swap), swap ? hi : lo);
+            st_shared_v4(op + op_offset(tok, 2 * u + !swap), swap ? lo : hi);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(bar_raw_empty);
+          bar_arrive(bar_full);
+        }
       }
-      ok = waiter.wait(bar_v_empty + 8 * st, empty) && waiter.wait(bar_rv_full + 8 * rs, full);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      decode(sbase + L::kRawV + rs * L::kRawBytes, sbase + L::kV + st * L::kOp);
-      if (lane == 0) {
-        bar_arrive(bar_rv_empty + 8 * rs);
-        bar_arrive(bar_v_full + 8 * st);
-      }
+      if (!ok) break;
     }
   } else {
     // ------------------------------------------------------------ MMA issuer
     fewer_regs<kMmaRegs>();
-    if (warp == kMmaWarp && n_tiles > 0) {
-      // the whole warp, so that operands are uniform; one lane issues
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        return __all_sync(0xFFFFFFFFu, waiter.wait(bar, parity));
-      };
-      bool ok = true;
-      for (int g = 0; g < n_q && ok; ++g) ok = wait(bar_q + 8 * g, 0);
+    // Two warps issue the MMAs, one S and one P V, so that the waits of one overlap the products
+    // of the other; a whole warp each, so that operands are uniform, one lane of which issues.
+    if ((warp == kMmaWarp || warp == kPvWarp) && n_tiles > 0) {
       // low descriptor words: K-major with LBO 1, MN-major with the chunk stride
       const uint32_t lo_k = ((sbase & 0x3FFFFu) >> 4) | (1u << 16);
       const uint32_t lo_mn = ((sbase & 0x3FFFFu) >> 4) | (uint32_t(kChunkBytes >> 4) << 16);
-      // S_g(j) = Q_g K_j^T: 16 dims a step, +32 bytes, the next chunk after 4
-      auto issue_s = [&](uint32_t g, int j) {
-        const uint32_t qd = lo_k + ((L::kQ + g * L::kOp) >> 4);
-        const uint32_t kd = lo_k + ((L::kK + (j % kStages) * L::kOp) >> 4);
-        unrolled(
-            [&](auto k) {
-              constexpr uint32_t at = (k.value >> 2) * (kChunkBytes >> 4) + 2 * (k.value & 3);
-              warp_mma_ss<at, at>(tmem + kSCol0 + 128 * g, qd, kd, idesc(kKeys), k.value != 0);
-            },
-            std::make_integer_sequence<uint32_t, kD / 16>());
-        warp_commit(bar_s_full + 8 * g);
-      };
-      // O_g += P_g(j) V_j, as the halves of P come: 16 keys a step, 8 columns of P
-      auto issue_pv = [&](uint32_t g, int j) {
-        const uint32_t vd = lo_mn + ((L::kV + (j % kStages) * L::kOp) >> 4);
-        const uint32_t od = tmem + kOCol0 + 128 * g, pd = tmem + kSCol0 + 128 * g;
-        if (!wait(bar_p_ready + 16 * g, j & 1)) return false;
-        tc_fence_after();
-        unrolled(
-            [&](auto k) {
-              warp_mma_ts<8 * k.value, k.value * (2048 >> 4)>(od, pd, vd, idesc(kD) | (1u << 16),
-                                                              k.value != 0 || j != 0);
-            },
-            std::make_integer_sequence<uint32_t, 4>());
-        if (!wait(bar_p_ready + 16 * g + 8, j & 1)) return false;
-        tc_fence_after();
-        unrolled(
-            [&](auto k) {
-              warp_mma_ts<32 + 8 * k.value, (4 + k.value) * (2048 >> 4)>(
-                  od, pd, vd, idesc(kD) | (1u << 16), 1);
-            },
-            std::make_integer_sequence<uint32_t, 4>());
-        warp_commit(bar_pv_done + 8 * g);
-        return true;
-      };
-      auto ready = [&](uint32_t bar, int j) {
-        if (!wait(bar + 8 * (j % kStages), (j / kStages) & 1)) return false;
-        tc_fence_after();
-        return true;
-      };
-      if (ok && (ok = ready(bar_k_full, 0))) {
-        for (int g = 0; g < n_q; ++g) issue_s(g, 0);
-        warp_commit(bar_k_empty);
-      }
-      for (int j = 0; j < n_tiles && ok; ++j) {
-        const bool more = j + 1 < n_tiles;
+      bool ok = true;
+      if (warp == kMmaWarp) {
+        // S = Q_g K_j^T, once the softmax before has read S: 16 dims a step, +32 bytes, the
+        // next chunk after 4
+        uint32_t issued = 0;
+        for (int g = 0; g < n_q && ok; ++g) ok = waiter.wait(bar_q + 8 * g, 0);
 #pragma unroll 1
-        for (int g = 0; g < n_q; ++g) {
-          const bool last = g == n_q - 1;
-          if (g == 0 && !(ok = ready(bar_v_full, j))) break;
-          if (!(ok = issue_pv(g, j))) break;
-          if (last) warp_commit(bar_v_empty + 8 * (j % kStages));
-          if (more) {
-            if (g == 0 && !(ok = ready(bar_k_full, j + 1))) break;
-            issue_s(g, j + 1);
-            if (last) warp_commit(bar_k_empty + 8 * ((j + 1) % kStages));
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          const uint32_t st = j % kStages;
+          if (!(ok = waiter.wait(bar_k_full + 8 * st, (j / kStages) & 1))) break;
+          const uint32_t kd = lo_k + ((L::kK + st * L::kOp) >> 4);
+#pragma unroll 1
+          for (int g = 0; g < n_q; ++g) {
+            if (issued > 0 && !(ok = waiter.wait(bar_s_free, (issued - 1) & 1))) break;
+            ++issued;
+            tc_fence_after();
+            const uint32_t qd = lo_k + ((L::kQ + g * L::kOp) >> 4);
+            unrolled(
+                [&](auto k) {
+                  constexpr uint32_t at = (k.value >> 2) * (kChunkBytes >> 4) + 2 * (k.value & 3);
+                  warp_mma_ss<at, at>(tmem + kSCol0, qd, kd, idesc(kKeys), k.value != 0);
+                },
+                std::make_integer_sequence<uint32_t, kD / 16>());
+            warp_commit(bar_s_full + 8 * g);
           }
+          if (ok) warp_commit(bar_k_empty + 8 * st);
         }
+      } else {
+        // O_g += P_g(j) V_j: 16 keys a step, 8 columns of P
+#pragma unroll 1
+        for (int j = 0; j < n_tiles && ok; ++j) {
+          const uint32_t st = j % kStages;
+          if (!(ok = waiter.wait(bar_v_full + 8 * st, (j / kStages) & 1))) break;
+          const uint32_t vd = lo_mn + ((L::kV + st * L::kOp) >> 4);
+#pragma unroll 1
+          for (int g = 0; g < n_q; ++g) {
+            const uint32_t od = tmem + kOCol0 + 128 * g, pd = tmem + kPCol0 + 64 * g;
+            if (!(ok = waiter.wait(bar_p_ready + 8 * g, j & 1))) break;
+            tc_fence_after();
+            unrolled(
+                [&](auto k) {
+                  warp_mma_ts<8 * k.value, k.value * (2048 >> 4)>(
+                      od, pd, vd, idesc(kD) | (1u << 16), k.value != 0 || j != 0);
+                },
+                std::make_integer_sequence<uint32_t, 8>());
+            warp_commit(bar_pv_done + 8 * g);
+          }
+          if (ok) warp_commit(bar_v_empty + 8 * st);
+        }
+        if (ok) warp_commit(bar_o_full);
       }
-      if (ok) warp_commit(bar_o_full);
       // drain: every tcgen05 operation this warp issued has completed
-      warp_commit(bar_drain);
+      const uint32_t drain = bar_drain + (warp == kMmaWarp ? 0 : 8);
+      warp_commit(drain);
       const uint64_t t0 = globaltimer();
-      while (!bar_try_wait(bar_drain, 0)) {
+      while (!bar_try_wait(drain, 0)) {
         if (globaltimer() - t0 > 2000000000ull) {
           record_status(a.status, NVFP4_ERR_TIMEOUT);
           break;
@@ -531,24 +608,28 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const int tok = t_begin + j * kKeys + 16 * lane;
         const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
         const int64_t at = ((int64_t(max(page, 0)) * a.kv_heads + h) * a.page_tokens + in_page) * kD;
-        const uint32_t live = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0));
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, page >= 0);
         bool ok = true;
 #pragma unroll
         for (int pl = 0; pl < 2 && ok; ++pl) {
           const uint32_t full = (pl ? bar_rv_full : bar_rk_full) + 8 * rs;
-          ok = __all_sync(0xFFFFFFFFu,
-                          waiter.wait((pl ? bar_rv_empty : bar_rk_empty) + 8 * rs, empty));
+          ok = waiter.wait((pl ? bar_rv_empty : bar_rk_empty) + 8 * rs, empty);
           if (!ok) break;
+          const uint32_t to = sbase + (pl ? L::kRawV : L::kRawK) + rs * L::kRawBytes;
+          // groups of no page are zero
+          for (uint32_t none = 0xFFu & ~have; none != 0; none &= none - 1)
+            for (uint32_t at = lane * 16; at < kBytes; at += 512)
+              st_shared_v4(to + (__ffs(none) - 1) * kBytes + at, make_uint4(0, 0, 0, 0));
+          __syncwarp();
           if (lane == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full),
-                         "r"(live * kBytes)
+                         "r"(__popc(have) * kBytes)
                          : "memory");
           __syncwarp();
           if (page >= 0)
             asm volatile(
                 "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], "
-                "%2, [%3];" ::"r"(sbase + (pl ? L::kRawV : L::kRawK) + rs * L::kRawBytes +
-                                  lane * kBytes),
+                "%2, [%3];" ::"r"(to + lane * kBytes),
                 "l"((pl ? a.v_codes : a.k_codes) + at), "r"(kBytes), "r"(full)
                 : "memory");
           __syncwarp();

@@ -702,7 +702,10 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   Kv8Plan p;
   const int32_t group = d.q_heads / d.kv_heads;
   const int64_t rows = int64_t(d.max_q) * group;
-  p.chunked = rows > 16;
+  // The tensor-core kernel from 33 packed rows on: its tiles have 128.  (8 x 5 queries of 4 heads
+  // over 3000 tokens, 20 rows: 33 us here, in two tiles of 16 rows, 40 there; 4 x 16 queries, 64
+  // rows: 33 and 29.)
+  p.chunked = rows > 32;
   p.rows = p.chunked ? 256 : rows <= 8 ? 8 : 16;
   p.row_tiles = int32_t((rows + p.rows - 1) / p.rows);
   // Ranges, none shorter than 128 tokens.  Few units: as many as fill one wave of three CTAs

@@ -509,3 +509,37 @@ def test_the_same_bits_every_time(nq):
     first = cache.attention(q, *args, max_q=nq)
     for _ in range(5):
         assert torch.equal(cache.attention(q, *args, max_q=nq), first)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_a_long_run_of_bad_pages_first(nq):
+    """Tiles without a single page before the real ones, whose weights are far from 1."""
+    c = _random_cache(8, 16, 1, 128, 23)
+    c.v_scale[:] = 2.0 ** -25
+    q = torch.randn(nq, 4, 128, generator=torch.Generator().manual_seed(2))
+    q = q.to(torch.bfloat16).cuda()
+    o, lse = c.attention(q, i32([0, nq]), i32([20 * 16]), i32([[-1] * 12 + list(range(8))]),
+                         causal=False, max_q=nq, return_lse=True)
+    assert nv.device_status() == N.ERR_INVALID_ARG
+    want = ref.attention(q.cpu().double(), *_planes64(c), [list(range(8))], [nq], [128], 16, False,
+                         128 ** -0.5)
+    ref.assert_attention_close(o, lse, want)
+
+
+@pytest.mark.parametrize("nq", [1, 130])
+@pytest.mark.parametrize("step", [0.5, 3.0, 40.0])
+def test_scores_that_rise_all_along(nq, step):
+    """Every tile has larger scores than the ones before: the reference is raised again and
+    again, by little and by much."""
+    c = _random_cache(64, 16, 1, 64, 24, spread=0)
+    c.k_codes.view(torch.uint8)[:] = 0x38                      # 1.0
+    for p in range(64):
+        c.k_scale[p] = 2.0 ** -6
+        c.k_codes.view(torch.uint8)[p, :, :, : p] = 0x40       # 2.0 in the first p dims
+    g = torch.Generator().manual_seed(3)
+    q = (torch.rand(nq, 2, 64, generator=g) * step * 8).to(torch.bfloat16).cuda()
+    o, lse = c.attention(q, i32([0, nq]), i32([1024]), i32([list(range(64))]), causal=False,
+                         max_q=nq, return_lse=True)
+    want = ref.attention(q.cpu().double(), *_planes64(c), [list(range(64))], [nq], [1024], 16,
+                         False, 0.125)
+    ref.assert_attention_close(o, lse, want)
