@@ -330,7 +330,7 @@ NVFP4_API int64_t nvfp4_sink_plan_frame_of_slot(const nvfp4_sink_plan* plan, int
  * Products are exact up to the representation of x (below), sums fp32.
  *   x:   device, bf16 or fp32 (x_dtype), m rows of W->cols values at stride ldx
  *        elements, 1 <= m <= NVFP4_GEMV_MAX_ROWS; 16-byte aligned, ldx * element size
- *        a multiple of 16 bytes.  Each row is taken, per 128 columns, relative to the
+ *        a multiple of 16 bytes.  Each row is taken, per 256 columns, relative to the
  *        largest magnitude there: bf16 values exactly down to 2^-22 of it and within
  *        2^-33 of it below; fp32 values within 2^-22 relative, or 2^-43 of it below.
  *   W:   N x K weights, either scale layout; K a multiple of 32.

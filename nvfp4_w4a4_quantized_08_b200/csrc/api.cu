@@ -408,7 +408,8 @@ nvfp4_status nvfp4_gemv(const void* x, int32_t x_dtype, int64_t m, int64_t ldx,
   if (act != NVFP4_ACT_NONE && act != NVFP4_ACT_GELU_TANH) return NVFP4_ERR_INVALID_ARG;
   if (m < 1 || ldx < W->cols || ldy < W->rows) return NVFP4_ERR_INVALID_ARG;
   if (m > NVFP4_GEMV_MAX_ROWS || W->cols % 32 != 0 || W->rows >= (int64_t(1) << 30) ||
-      W->cols >= (int64_t(1) << 30))
+      W->cols >= (int64_t(1) << 30) ||
+      nvfp4_sf_bytes(W->rows, W->cols, W->sf_layout) >= (size_t(1) << 31))
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   const int64_t xsz = x_dtype == NVFP4_BF16 ? 2 : 4, ysz = y_dtype == NVFP4_BF16 ? 2 : 4;
   if (!aligned(x, 16) || (ldx * xsz) % 16 != 0 || !aligned(y, uintptr_t(ysz)))

@@ -9,29 +9,35 @@
 // code and row); so the codes go through the tensor cores as fp16:
 //   - v(q) s_b is exact in fp16: a 2-bit times a 4-bit significand, magnitudes
 //     2^-10 .. 2688.  One hardware conversion per two codes, one packed multiply.
-//   - x is scaled by a power of two per row and 128 columns to magnitudes below
+//   - x is scaled by a power of two per row and 256 columns to magnitudes below
 //     2^9 and converted to fp16: exact for bf16 values within 2^-22 of the
-//     largest of the 128, below that an error of at most 2^-33 of the largest.
+//     largest of the 256, below that an error of at most 2^-33 of the largest.
 //     fp32 x takes two fp16 parts (the second is the remainder times 2^11) in
 //     two columns of the product, 22 bits together.
 //   - m16n8k16 with fp32 accumulation: 16 weight rows by 8 columns, the columns
-//     being the rows of x (or their parts).  The 8 products of a 128-column step
+//     being the rows of x (or their parts).  The 16 products of a 256-column step
 //     start from zero and are joined to the fp32 sum by one FMA with the step's
-//     power of two, which also bounds the tensor core's truncation to 8 sums.
+//     power of two, which also bounds the tensor core's truncation to 16 sums.
 // The order of the 16 columns inside one product is free as long as both
-// operands use the same one, so a thread's 16-byte load of codes (32 columns,
-// two scale blocks) feeds 8 products without any exchange between threads.
+// operands use the same one, so a thread's 32 bytes of codes (64 columns, four
+// scale blocks) feed 16 products without any exchange between threads.
 //
-// A CTA has 8 warps: KW of them split the columns (steps dealt out in turn),
-// the other factor 8 / KW takes further rows, which then share the converted x.
-// KW falls with the rows of x (8 warps convert at most 16 row-steps at a time),
-// so the conversion stays a small part of the work.  The 16 weight rows of a
-// warp are 4 i-values by 4 rows 32 apart: the scale tile of the tensor-core
-// layout keeps exactly their scales in 64 contiguous bytes.  Where rows alone
-// leave SMs idle, a cluster of up to 8 CTAs splits the columns again and joins
-// the sums through distributed shared memory in rank order: no workspace, no
-// atomics, the same result every time.
+// A warp takes steps of 32 weight rows by 256 columns (16 rows for the widest x): 128 bytes, a
+// whole line, of each row, copied asynchronously into a ring of its own two steps deep.  (Loads
+// straight into registers, 64 bytes of a row at a time and 16 rows a warp, took 17.4 us for
+// 14336 x 4096 and one row, 13.7 with 32 rows; this takes 11.5, 2.9 TB/s.  Three steps deep
+// leaves one CTA an SM: 17 us.)  A CTA has 8 warps: KW of them split the columns (steps dealt out in turn), the
+// other factor 8 / KW takes further rows, which then share the converted x; KW falls with the
+// rows of x, so that the conversion stays a small part of the work.  With KW = 8 a warp
+// converts what it reads itself, and no barrier is needed.  (Converting all of x first, in
+// a prologue, cost 0.7 us at 1024 x 1024.)  The 16 weight rows of a product are 4 i-values by
+// 4 rows 32 apart: the scale tile of the tensor-core layout keeps their scales in 64
+// contiguous bytes.  Where rows alone leave SMs idle, a cluster of up to 8 CTAs splits the
+// columns again and joins the sums through distributed shared memory in rank order: no
+// workspace, no atomics, the same result every time.
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -41,9 +47,9 @@ namespace gemv {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 128;         // columns a warp takes at a time
-constexpr int kDepth = 4;          // steps of weight loads in flight per warp
-constexpr int kXRow = 320;         // bytes of one converted row-step: 256 and a bank offset
+constexpr int kStep = 256;         // columns a warp takes at a time
+constexpr int kStages = 2;         // steps of weights in a warp's ring
+constexpr int kXRow = 576;         // bytes of one converted row-step: 512 and a bank offset
 constexpr int kMaxCluster = 8;
 
 struct Args {
@@ -57,6 +63,7 @@ struct Args {
   int32_t M, N, K;
   int32_t sf_tiled;       // tensor-core layout of the scales (else row-major)
   int32_t y_bf16, act;
+  FastDiv m_div;
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -79,6 +86,20 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
+// 16 bytes to shared memory, zeros where `bytes` is 0.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at));
+  return v;
+}
+
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -96,17 +117,35 @@ __device__ __forceinline__ float gelu_tanh(float y) {
   return 0.5f * y * (1.0f + tanhf(u));
 }
 
+// Products of 16 weight rows per warp (one where four tiles of columns fill the registers).
+template <int NT>
+constexpr int kRowTiles = NT < 4 ? 2 : 1;
+
+// Shared memory: the rings, or after the last step the warps' sums; then KW M <= 16 row-steps
+// of x, twice.
+template <int NT>
+constexpr int kRingBytes = std::max(kWarps * kStages * kRowTiles<NT> * 16 * (kStep / 2),
+                                    kWarps * kRowTiles<NT> * 16 * (NT * 8 + 1) * 4);
+template <bool FP32>
+constexpr int kXBytes = 2 * 16 * (FP32 ? 2 : 1) * kXRow;
+
 // KW warps split the columns; NT tiles of 8 product columns; FP32 x in two parts.
 template <int KW, int NT, bool FP32>
 __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
   namespace cg = cooperative_groups;
-  constexpr int RG = kWarps / KW;          // row groups of 16 weight rows
+  constexpr int kTiles = kRowTiles<NT>;
+  constexpr int RG = kWarps / KW;          // groups of 16 kTiles weight rows
+  constexpr int kOf128 = 8 / kTiles;       // groups of a 128-row tile
   constexpr int kPairs = 16;               // row-steps converted at a time (KW M <= 16)
+  constexpr int kPasses = kPairs / kWarps; // of them by one warp
   constexpr int kParts = FP32 ? 2 : 1;
   constexpr int kCols = NT * 8;
-  __shared__ alignas(16) uint8_t xs[2][kPairs * kParts * kXRow];
+  constexpr int kStage = kTiles * 16 * (kStep / 2);   // bytes of weights
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float xe[2][kPairs];          // power of two of each row-step
-  __shared__ float red[kWarps][16][kCols + 1];
+  // the rings, and after the last step the warps' sums in their place; then converted x
+  float (*red)[kTiles * 16][kCols + 1] = reinterpret_cast<float (*)[kTiles * 16][kCols + 1]>(smem);
+  uint8_t* xs = smem + (kRingBytes<NT> + 15) / 16 * 16;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kw = warp % KW, rg = warp / KW;
@@ -117,212 +156,291 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
   const int n_steps = (a.K + kStep - 1) / kStep;
   const int stride = KW * cs;                          // steps between a warp's own
   const int iters = (n_steps + stride - 1) / stride;   // the same for every CTA of a cluster
-
-  // weight row of tensor-core row rho: 4 g + rho % 4 + 32 (rho / 4) of its 128-row tile
-  const int group = group0 + rg;
-  const int row0 = (group >> 3) * 128 + (group & 7) * 4 + (r & 3) + 32 * (r >> 2);
-  const int ra = min(row0, a.N - 1), rb = min(row0 + 64, a.N - 1);
-  const int64_t pitch = a.K / 2;
-  const uint8_t* wa = a.codes + ra * pitch + 16 * c;
-  const uint8_t* wb = a.codes + rb * pitch + 16 * c;
-  const uint8_t *sa, *sb;
-  int64_t s_step;
-  if (a.sf_tiled) {
-    const int64_t tiles = (a.K / 16 + 3) / 4;
-    auto at = [&](int row) {
-      return a.sf + (int64_t(row >> 7) * tiles + (c >> 1)) * 512 + (row & 31) * 16 +
-             ((row >> 5) & 3) * 4 + (c & 1) * 2;
-    };
-    sa = at(ra);
-    sb = at(rb);
-    s_step = 1024;
-  } else {
-    sa = a.sf + int64_t(ra) * (a.K / 16) + 2 * c;
-    sb = a.sf + int64_t(rb) * (a.K / 16) + 2 * c;
-    s_step = 8;
-  }
   const int first = rank * KW + kw;
+  const int group = group0 + rg;
 
-  pdl_wait();
-  pdl_trigger();
-
-  uint4 wq[kDepth][2];
-  uint32_t sq[kDepth][2];
-  // step i of this warp: columns [128 s + 32 c, + 32) are all inside K or all outside
-  auto load_w = [&](int i, uint4 (&w)[2], uint32_t (&s)[2]) {
-    const int st = first + i * stride;
-    if (st * kStep + 32 * c < a.K) {
-      w[0] = ld_nc_v4(wa + int64_t(st) * (kStep / 2));
-      w[1] = ld_nc_v4(wb + int64_t(st) * (kStep / 2));
-      s[0] = __ldg(reinterpret_cast<const uint16_t*>(sa + st * s_step));
-      s[1] = __ldg(reinterpret_cast<const uint16_t*>(sb + st * s_step));
-    } else {
-      w[0] = w[1] = make_uint4(0, 0, 0, 0);
-      s[0] = s[1] = 0;
-    }
+  // weight row of row rho of product t: 4 (kTiles g + t) + rho % 4 + 32 (rho / 4) of a
+  // 128-row tile
+  auto row_of = [&](int t, int rho) {
+    return min(group / kOf128 * 128 + (kTiles * (group % kOf128) + t) * 4 + (rho & 3) +
+                   32 * (rho >> 2),
+               a.N - 1);
   };
+  // copies: lane l takes 16-byte unit l % 8 of rows l / 8 + 4 i; units exchanged by the row's
+  // place, so that the reads below meet no bank twice
+  const int64_t pitch = a.K / 2;
+  const uint8_t* from[kTiles * 4];
+  uint32_t to[4];
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
+                        uint32_t(warp) * kStages * kStage;
 #pragma unroll
-  for (int i = 0; i < kDepth; ++i) load_w(i, wq[i], sq[i]);
+  for (int i = 0; i < 4; ++i) {
+    const int rho = lane / 8 + 4 * i;
+    to[i] = ring + rho * 128 + (((lane & 7) ^ (rho & 7)) << 4);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+      from[4 * t + i] = a.codes + row_of(t, rho) * pitch + 16 * (lane & 7);
+  }
+  auto issue = [&](int i) {   // step i of this warp
+    const int st = first + i * stride;
+    if (i < iters && st < n_steps) {
+      const uint32_t in = st * kStep + 32 * (lane & 7) < a.K ? 16 : 0;
+      const uint32_t stage = uint32_t(i % kStages) * kStage;
+      const int64_t at = in ? int64_t(st) * (kStep / 2) : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+          copy16(to[j] + stage + t * 16 * (kStep / 2), from[4 * t + j] + at, in);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // scales: the four of blocks 4 c .. 4 c + 3 of rows r and r + 8, two steps ahead
+  int32_t s_at[kTiles][2];
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = row_of(t, r + 8 * i);
+      s_at[t][i] = a.sf_tiled ? ((row >> 7) * ((a.K / 16 + 3) / 4) + c) * 512 + (row & 31) * 16 +
+                                    ((row >> 5) & 3) * 4
+                              : row * (a.K / 16) + 4 * c;
+    }
+  auto load_s = [&](int i, uint32_t (&sc)[kTiles][2]) {
+    const int st = first + i * stride;
+    const int left = i < iters ? a.K / 16 - st * (kStep / 16) - 4 * c : 0;   // blocks (even)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sc[t][j] = 0;
+        if (left > 0) {
+          if (a.sf_tiled) {   // (padded to whole tiles with zeros)
+            sc[t][j] = __ldg(reinterpret_cast<const uint32_t*>(a.sf + s_at[t][j] + st * 2048));
+          } else {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(a.sf + s_at[t][j] + st * 16);
+            sc[t][j] = __ldg(p);
+            if (left > 2) sc[t][j] |= uint32_t(__ldg(p + 1)) << 16;
+          }
+        }
+      }
+  };
 
-  // conversion: half warp p takes row-step p = kw' * M + m, thread u its columns 8 u ..
-  const int pair = tid >> 4, u = tid & 15;
-  const int cv_kw = pair / a.M, cv_m = pair % a.M;
-  const bool cv = cv_kw < KW;
-  uint4 xv[kParts];
+  // conversion: a warp takes a row-step, 8 columns a lane.  With KW = 8 its own step's rows, else
+  // row-steps `warp` and `warp + 8` of the CTA's.
+  struct Eight {
+    uint4 v[kParts];
+  };
+  Eight xv[kPasses];
+  auto pair_of = [&](int p, int& step_of, int& m) {
+    const int pair = warp + kWarps * p;
+    step_of = KW == kWarps ? kw : int(fast_div(a.m_div, uint32_t(pair)));
+    m = KW == kWarps ? p : pair - step_of * a.M;
+    return KW == kWarps ? p < a.M : step_of < KW;
+  };
   auto load_x = [&](int i) {
-    const int col = (rank * KW + cv_kw + i * stride) * kStep + 8 * u;
-    xv[0] = make_uint4(0, 0, 0, 0);
-    if constexpr (FP32) xv[1] = xv[0];
-    if (cv && i < iters && col < a.K) {
-      if constexpr (FP32) {
-        const float* p = static_cast<const float*>(a.x) + cv_m * a.ldx + col;
-        xv[0] = ld_nc_v4_l1(p);
-        xv[1] = ld_nc_v4_l1(p + 4);
-      } else {
-        xv[0] = ld_nc_v4_l1(static_cast<const uint16_t*>(a.x) + cv_m * a.ldx + col);
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      int step_of, m;
+      const bool on = pair_of(p, step_of, m);
+      const int col = (rank * KW + step_of + i * stride) * kStep + 8 * lane;
+#pragma unroll
+      for (int e = 0; e < kParts; ++e) xv[p].v[e] = make_uint4(0, 0, 0, 0);
+      if (on && i < iters && col < a.K) {
+        if constexpr (FP32) {
+          const float* x = static_cast<const float*>(a.x) + m * a.ldx + col;
+          xv[p].v[0] = ld_nc_v4_l1(x);
+          xv[p].v[1] = ld_nc_v4_l1(x + 4);
+        } else {
+          xv[p].v[0] = ld_nc_v4_l1(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
+        }
       }
     }
   };
   auto convert_x = [&](int buf) {
-    float f[8];
-    if constexpr (FP32) {
-      f[0] = __uint_as_float(xv[0].x); f[1] = __uint_as_float(xv[0].y);
-      f[2] = __uint_as_float(xv[0].z); f[3] = __uint_as_float(xv[0].w);
-      f[4] = __uint_as_float(xv[1].x); f[5] = __uint_as_float(xv[1].y);
-      f[6] = __uint_as_float(xv[1].z); f[7] = __uint_as_float(xv[1].w);
-    } else {
-      const uint32_t w[4] = {xv[0].x, xv[0].y, xv[0].z, xv[0].w};
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+      int step_of, m;
+      if (!pair_of(p, step_of, m)) continue;   // the same for the whole warp
+      float f[8];
+      const uint4 v0 = xv[p].v[0];
+      if constexpr (FP32) {
+        const uint4 v1 = xv[p].v[1];
+        f[0] = __uint_as_float(v0.x); f[1] = __uint_as_float(v0.y);
+        f[2] = __uint_as_float(v0.z); f[3] = __uint_as_float(v0.w);
+        f[4] = __uint_as_float(v1.x); f[5] = __uint_as_float(v1.y);
+        f[6] = __uint_as_float(v1.z); f[7] = __uint_as_float(v1.w);
+      } else {
+        const uint32_t w[4] = {v0.x, v0.y, v0.z, v0.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = __uint_as_float(w[i] << 16);
+          f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      // 2^e with max |x| 2^e in [2^8, 2^9), kept where its inverse is normal too
+      const uint32_t field = min(262u - (top >> 23), 253u);
+      const float scale = __uint_as_float(field << 23);
+      uint32_t hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        const float u = f[2 * i] * scale, v = f[2 * i + 1] * scale;
+        hi[i] = f16x2_rn(u, v);
+        if constexpr (FP32) {
+          const __half2 h = *reinterpret_cast<const __half2*>(&hi[i]);
+          lo[i] = f16x2_rn((u - __low2float(h)) * 2048.0f, (v - __high2float(h)) * 2048.0f);
+        }
       }
-    }
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(f[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    // 2^e with max |x| 2^e in [2^8, 2^9), kept where its inverse is normal too
-    const uint32_t field = min(262u - (top >> 23), 253u);
-    const float scale = __uint_as_float(field << 23);
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float p = f[2 * i] * scale, q = f[2 * i + 1] * scale;
-      hi[i] = f16x2_rn(p, q);
-      if constexpr (FP32) {
-        const __half2 h = *reinterpret_cast<const __half2*>(&hi[i]);
-        lo[i] = f16x2_rn((p - __low2float(h)) * 2048.0f, (q - __high2float(h)) * 2048.0f);
-      }
-    }
-    if (cv) {
-      const uint32_t at = ((u & 3) * 4 + (u >> 2)) * 16;
-      uint8_t* d = xs[buf] + (cv_kw * a.M + cv_m) * kParts * kXRow + at;
+      // columns 64 c + 8 q .. of a step (lane 8 c + q): unit 4 q + c of its row, so that the
+      // reads below, lanes c of one q, are 64 contiguous bytes
+      const int pair = step_of * a.M + m;
+      uint8_t* d = xs + (buf * kPairs + pair) * kParts * kXRow + ((lane & 7) * 4 + (lane >> 3)) * 16;
       *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if constexpr (FP32)
         *reinterpret_cast<uint4*>(d + kXRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      if (u == 0) xe[buf][cv_kw * a.M + cv_m] = __uint_as_float((254u - field) << 23);
+      if (lane == 0) xe[buf][pair] = __uint_as_float((254u - field) << 23);
     }
   };
 
-  float acc[NT][4];
+  float acc[kTiles][NT][4];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+  for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][n][i] = 0.0f;
   const int cols = a.M * kParts;   // product column n: row n / kParts, part n % kParts
 
-  auto step = [&](int buf, const uint4 (&w)[2], const uint32_t (&s)[2]) {
-    float d[NT][4];
+  auto step = [&](int i, int buf, const uint32_t (&sc)[kTiles][2]) {
+    float d[kTiles][NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[t][i] = 0.0f;
-    // the two block scales of each weight row, both halves of a pair
-    uint32_t s2[2][2];
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t h;
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)s[i]));
-      s2[i][0] = prmt(h, h, 0x1010);
-      s2[i][1] = prmt(h, h, 0x3232);
-    }
-    const uint32_t wa4[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-    const uint32_t wb4[4] = {w[1].x, w[1].y, w[1].z, w[1].w};
-    const uint8_t* xb = xs[buf] + kw * cols * kXRow + c * 16;
+        for (int j = 0; j < 4; ++j) d[t][n][j] = 0.0f;
+    const uint32_t stage = ring + uint32_t(i % kStages) * kStage;
+    const uint8_t* xb = xs + (buf * kPairs + kw * a.M) * kParts * kXRow + c * 16;
+    // halves of a lane's 32 bytes: two scale blocks, 8 products each
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t ha[4], hb[4];
-      codes_f16(wa4[q], ha);
-      codes_f16(wb4[q], hb);
+    for (int half = 0; half < 2; ++half) {
+      uint4 w[kTiles][2];
+      uint32_t s2[kTiles][2][2];   // the block scales of rows r and r + 8, both halves of a pair
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ha[i] = mul_f16x2(ha[i], s2[0][q >> 1]);
-        hb[i] = mul_f16x2(hb[i], s2[1][q >> 1]);
+      for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t rho = r + 8 * j;
+          w[t][j] = lds16(stage + t * 16 * (kStep / 2) + rho * 128 +
+                          (((2 * c + half) ^ (rho & 7)) << 4));
+          uint32_t h;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
+              : "=r"(h)
+              : "h"((unsigned short)(sc[t][j] >> (16 * half))));
+          s2[t][j][0] = prmt(h, h, 0x1010);
+          s2[t][j][1] = prmt(h, h, 0x3232);
+        }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint4 b[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          b[n] = make_uint4(0, 0, 0, 0);
+          if (8 * n + r < cols)
+            b[n] = *reinterpret_cast<const uint4*>(xb + (8 * n + r) * kXRow + (4 * half + k) * 64);
+        }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          uint32_t h[2][4];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4& q = w[t][j];
+            codes_f16(k == 0 ? q.x : k == 1 ? q.y : k == 2 ? q.z : q.w, h[j]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[j][e] = mul_f16x2(h[j][e], s2[t][j][k >> 1]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(d[t][n], h[0][0], h[1][0], h[0][1], h[1][1], b[n].x, b[n].y);
+            mma_f16(d[t][n], h[0][2], h[1][2], h[0][3], h[1][3], b[n].z, b[n].w);
+          }
+        }
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        uint4 b = make_uint4(0, 0, 0, 0);
-        if (8 * t + r < cols)
-          b = *reinterpret_cast<const uint4*>(xb + (8 * t + r) * kXRow + q * 64);
-        mma_f16(d[t], ha[0], hb[0], ha[1], hb[1], b.x, b.y);
-        mma_f16(d[t], ha[2], hb[2], ha[3], hb[3], b.z, b.w);
-      }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int n0 = 8 * t + 2 * c;
+    for (int n = 0; n < NT; ++n) {
+      const int n0 = 8 * n + 2 * c;
       const float* e = xe[buf] + kw * a.M;
       const float e0 = n0 < cols ? e[n0 / kParts] : 0.0f;
       const float e1 = n0 + 1 < cols ? e[(n0 + 1) / kParts] : 0.0f;
-      acc[t][0] = fmaf(d[t][0], e0, acc[t][0]);
-      acc[t][1] = fmaf(d[t][1], e1, acc[t][1]);
-      acc[t][2] = fmaf(d[t][2], e0, acc[t][2]);
-      acc[t][3] = fmaf(d[t][3], e1, acc[t][3]);
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) {
+        acc[t][n][0] = fmaf(d[t][n][0], e0, acc[t][n][0]);
+        acc[t][n][1] = fmaf(d[t][n][1], e1, acc[t][n][1]);
+        acc[t][n][2] = fmaf(d[t][n][2], e0, acc[t][n][2]);
+        acc[t][n][3] = fmaf(d[t][n][3], e1, acc[t][n][3]);
+      }
     }
   };
 
+  pdl_wait();
+  pdl_trigger();
   load_x(0);
-  for (int i0 = 0; i0 < iters; i0 += kDepth) {
 #pragma unroll
-    for (int j = 0; j < kDepth; ++j) {
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  uint32_t sc[2][kTiles][2];
+  load_s(0, sc[0]);
+  load_s(1, sc[1]);
+  for (int i0 = 0; i0 < iters; i0 += 2) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
       const int i = i0 + j;
       if (i < iters) {
-        convert_x(j & 1);
+        convert_x(j);
         load_x(i + 1);
-        // one barrier a step: buffer j & 1 is written again two steps on, after
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        // the step's weights and x are there; x's buffer j is written again two steps on, after
         // the next barrier, which every reader of this step has then passed
-        __syncthreads();
-        step(j & 1, wq[j], sq[j]);
-        load_w(i + kDepth, wq[j], sq[j]);
+        if constexpr (KW == kWarps) __syncwarp(); else __syncthreads();
+        issue(i + kStages - 1);
+        if (first + i * stride < n_steps) step(i, j, sc[j]);
+        load_s(i + 2, sc[j]);
       }
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();   // the rings are free for the sums
 
   // sums of the warps that split the columns, then of the cluster's CTAs
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    red[warp][r][8 * t + 2 * c] = acc[t][0];
-    red[warp][r][8 * t + 2 * c + 1] = acc[t][1];
-    red[warp][r + 8][8 * t + 2 * c] = acc[t][2];
-    red[warp][r + 8][8 * t + 2 * c + 1] = acc[t][3];
-  }
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      red[warp][16 * t + r][8 * n + 2 * c] = acc[t][n][0];
+      red[warp][16 * t + r][8 * n + 2 * c + 1] = acc[t][n][1];
+      red[warp][16 * t + r + 8][8 * n + 2 * c] = acc[t][n][2];
+      red[warp][16 * t + r + 8][8 * n + 2 * c + 1] = acc[t][n][3];
+    }
   if (cs > 1) cluster.sync(); else __syncthreads();
   const float st = __ldg(a.s_t);
-  for (int o = rank * kThreads + tid; o < RG * 16 * a.M; o += kThreads * cs) {
-    // consecutive threads: the 4 RG consecutive weight rows of each 32
-    const int i4 = o % (4 * RG), q = (o / (4 * RG)) & 3, m = o / (16 * RG);
-    const int g = i4 >> 2, rho = (i4 & 3) + 4 * q;
+  for (int o = rank * kThreads + tid; o < RG * kTiles * 16 * a.M; o += kThreads * cs) {
+    // consecutive threads: the 4 kTiles RG consecutive weight rows of each 32
+    constexpr int kRun = 4 * kTiles * RG;
+    const int i4 = o % kRun, q = (o / kRun) & 3, m = o / (4 * kRun);
+    const int g = i4 / (4 * kTiles), rho = 16 * ((i4 >> 2) % kTiles) + (i4 & 3) + 4 * q;
     const int grp = group0 + g;
-    const int n = (grp >> 3) * 128 + (grp & 7) * 4 + (i4 & 3) + 32 * q;
+    const int n = grp / kOf128 * 128 + grp % kOf128 * (4 * kTiles) + i4 % (4 * kTiles) + 32 * q;
     float sum = 0.0f;
     for (int k = 0; k < cs; ++k) {
       const float* base =
           cs > 1 ? cluster.map_shared_rank(&red[0][0][0], k) : &red[0][0][0];
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
-        const float* p = base + ((g * KW + w) * 16 + rho) * (kCols + 1) + m * kParts;
+        const float* p = base + ((g * KW + w) * kTiles * 16 + rho) * (kCols + 1) + m * kParts;
         float v = p[0];
         if constexpr (FP32) v = fmaf(p[1], 0x1p-11f, v);
         sum += v;
@@ -345,15 +463,19 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
 template <int KW, int NT, bool FP32>
 cudaError_t launch(const Args& a, int sm_count, cudaStream_t st) {
   constexpr int RG = kWarps / KW;
-  const int groups = (a.N + 127) / 128 * 8;
-  const int ctas = groups / RG;
+  const int groups = (a.N + 127) / 128 * (8 / kRowTiles<NT>);
+  const int ctas = (groups + RG - 1) / RG;
   const int n_steps = (a.K + kStep - 1) / kStep;
-  // split the columns over a cluster while that leaves every CTA two steps a warp and
-  // the grid within two CTAs an SM
-  int cs = 1;
-  while (cs < kMaxCluster && ctas * cs * 2 <= 2 * sm_count && n_steps >= KW * cs * 4) cs *= 2;
+  // Split the columns over a cluster while every warp has a step and every CTA an SM of its own
+  // (7 x 5000 x 14336: 31 us in 120 CTAs, 37 in 160 to 240, 67 in 40; 1 x 1024 x 12800: 6.1 us in
+  // 128, 7.3 in 256, 9.7 in 32).
+  int cs = std::min(kMaxCluster, std::max(1, sm_count / ctas));
+  cs = std::min(cs, std::max(1, n_steps / KW));
+  constexpr size_t kSmem = (kRingBytes<NT> + 15) / 16 * 16 + kXBytes<FP32>;
+  const cudaError_t e = allow_smem<gemv_kernel<KW, NT, FP32>>(kSmem);
+  if (e != cudaSuccess) return e;
   return launch_pdl_cluster(gemv_kernel<KW, NT, FP32>, dim3(unsigned(ctas * cs)),
-                            dim3(unsigned(cs)), dim3(kThreads), 0, st, a);
+                            dim3(unsigned(cs)), dim3(kThreads), kSmem, st, a);
 }
 
 }  // namespace gemv
@@ -373,14 +495,18 @@ cudaError_t launch_gemv(const LaunchGemv& g, cudaStream_t st) {
   a.sf_tiled = g.sf_layout == NVFP4_SF_MMA128x4;
   a.y_bf16 = g.y_dtype == NVFP4_BF16;
   a.act = g.act;
-  // KW M <= 16 row-steps are converted at a time; 8 NT >= product columns
+  a.m_div = make_fastdiv(uint32_t(a.M));
+  // KW M <= 16 row-steps are converted at a time; 8 NT >= product columns.  One or two rows over
+  // more weights than two CTAs an SM take with all warps on one group: 64 rows a CTA (1 x 14336 x
+  // 4096: 11.5 us against 12.2; 1 x 9216 x 5120, which fits, 9.9 against 7.8).
+  const bool many = (g.N + 31) / 32 > 2 * g.sm_count;
   if (g.x_dtype == NVFP4_BF16) {
-    if (g.M <= 2) return gemv::launch<8, 1, false>(a, g.sm_count, st);
+    if (g.M <= 2 && !many) return gemv::launch<8, 1, false>(a, g.sm_count, st);
     if (g.M <= 4) return gemv::launch<4, 1, false>(a, g.sm_count, st);
     if (g.M <= 8) return gemv::launch<2, 1, false>(a, g.sm_count, st);
     return gemv::launch<1, 2, false>(a, g.sm_count, st);
   }
-  if (g.M <= 2) return gemv::launch<8, 1, true>(a, g.sm_count, st);
+  if (g.M <= 2 && !many) return gemv::launch<8, 1, true>(a, g.sm_count, st);
   if (g.M <= 4) return gemv::launch<4, 1, true>(a, g.sm_count, st);
   if (g.M <= 8) return gemv::launch<2, 2, true>(a, g.sm_count, st);
   return gemv::launch<1, 4, true>(a, g.sm_count, st);
