@@ -1,4 +1,5 @@
-"""Build libnvfp4.so in-tree with nvcc for sm_100a (cross-compiles without a GPU).
+"""Build libnvfp4.so in-tree with nvcc for sm_100a (cross-compiles without a GPU), and the
+torch binding beside it with the host compiler.
 
     python -m nvfp4_w4a4_quantized_08_b200.build [--verbose]
 """
@@ -12,6 +13,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [
@@ -33,14 +35,44 @@ def deps():
                               [os.path.join(os.path.dirname(HERE), "include", "nvfp4.h")])
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def _newer(out: str, inputs) -> bool:
+    if not os.path.exists(out):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(f) <= t for f in deps())
+    t = os.path.getmtime(out)
+    return all(os.path.getmtime(f) <= t for f in inputs)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB, deps())
+
+
+def build_binding(force: bool = False) -> str:
+    src = os.path.join(CSRC, "binding.cpp")
+    header = os.path.join(os.path.dirname(HERE), "include", "nvfp4.h")
+    if not force and _newer(BINDING, [src, header]):
+        return BINDING
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    includes = cpp_extension.include_paths() + [
+        sysconfig.get_paths()["include"],
+        os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-isystem{i}" for i in includes], src, "-o", tmp, f"-L{lib_dir}",
+           f"-Wl,-rpath,{lib_dir}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-ldl"]
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

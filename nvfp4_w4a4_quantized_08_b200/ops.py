@@ -1,7 +1,8 @@
 """torch-facing wrappers of the libnvfp4 entry points.
 
 Argument marshalling only: each function passes device pointers, sizes and
-``torch.cuda.current_stream()`` to the C ABI, which launches the kernels.  No
+``torch.cuda.current_stream()`` to the C ABI, which launches the kernels: through
+ctypes, or where a kernel takes a few microseconds through csrc/binding.cpp.  No
 step of the NVFP4 path runs in Python or torch.
 """
 from __future__ import annotations
@@ -236,33 +237,22 @@ class KVCache:
         return out
 
 
-def _launch(fn, what: str, device: torch.device, *args) -> None:
-    """Calls an entry point on `device`'s current stream, with `device` current."""
-    if device.type != "cuda":
-        raise ValueError(f"{what} takes CUDA tensors")
-    i = device.index
-    if i == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
-    if status:
-        raise NVFP4Error(status, what)
+_binding = None
 
 
-def _check_int32(device: torch.device, name: str, t: torch.Tensor, dims: int = 1) -> None:
-    if t.dtype is not torch.int32 or t.device != device or t.dim() != dims:
-        raise ValueError(f"{name} must be an int32 tensor of {dims} dimension(s) on {device}")
-    if dims == 1:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    elif t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have unit column stride")
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """The row stride of a 2-D tensor; torch gives any number for a single row."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _load_binding():
+    """The compiled module behind gemv, plan_pages and KVCache8, whose kernels take
+    less time than a ctypes call; it calls the entry points of the same library."""
+    global _binding
+    N.lib()  # raises if the library has not been built
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        raise RuntimeError("the torch binding has not been built for this torch; run python -m "
+                           f"nvfp4_w4a4_quantized_08_b200.build ({e})") from e
+    b.init(N.LIB_PATH, NVFP4Error, workspace)
+    _binding = b
+    return b
 
 
 def gemv(x: torch.Tensor, w: NVFP4Tensor, out_dtype: torch.dtype = torch.bfloat16,
@@ -270,21 +260,8 @@ def gemv(x: torch.Tensor, w: NVFP4Tensor, out_dtype: torch.dtype = torch.bfloat1
     """nvfp4_gemv: act(x W^T) for 1 to 16 rows x (bf16 or fp32, unit column
     stride) that are not quantized, and NVFP4 weights -> [x.rows, w.rows] in
     bf16 or fp32.  For more rows quantize x and use gemm."""
-    if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != w.cols:
-        raise ValueError(f"gemv expects a 2-D tensor of {w.cols} unit-stride columns")
-    if x.device != w.device:
-        raise ValueError("x and w must be on one device")
-    if out is None:
-        out = torch.empty((x.shape[0], w.rows), dtype=out_dtype, device=x.device)
-    elif (out.dim() != 2 or out.shape[0] != x.shape[0] or out.shape[1] < w.rows or
-          out.stride(1) != 1 or out.device != x.device):
-        raise ValueError(f"out must have {x.shape[0]} rows of at least {w.rows} unit-stride "
-                         f"columns on {x.device}")
-    sw = w.c_struct()
-    _launch(N.lib().nvfp4_gemv, "nvfp4_gemv", x.device, x.data_ptr(), _dtype_code(x), x.shape[0],
-            _row_stride(x), ctypes.byref(sw), out.data_ptr(), _dtype_code(out), _row_stride(out),
-            act)
-    return out
+    return (_binding or _load_binding()).gemv(x, w.codes, w.sf, w.s_t, w.rows, w.cols,
+                                              w.sf_layout, out_dtype, out, act)
 
 
 @dataclass
@@ -303,30 +280,9 @@ def plan_pages(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     device.  block_table [batch, max_pages] is updated in place; the rest are
     new tensors (free_head of the result goes into the next call).  Lengths that
     do not fit are reported by device_status, and then change nothing."""
-    dev = block_table.device
-    _check_int32(dev, "cached_lens", cached_lens)
-    _check_int32(dev, "new_lens", new_lens)
-    _check_int32(dev, "block_table", block_table, 2)
-    _check_int32(dev, "free_pages", free_pages)
-    _check_int32(dev, "free_head", free_head)
-    batch, max_pages = block_table.shape
-    if cached_lens.shape[0] != batch or new_lens.shape[0] != batch or free_head.shape[0] != 1:
-        raise ValueError("plan_pages: cached_lens and new_lens must be [batch], block_table "
-                         "[batch, max_pages], free_head [1]")
-    if max_new < 0:
-        raise ValueError("max_new must not be negative")
-    # one allocation for the four results, each on a 16-byte boundary
-    a, b = (batch + 3) // 4 * 4, (batch + 4) // 4 * 4
-    mem = torch.empty(4 + a + b + max_new, dtype=torch.int32, device=dev)
-    head, seq, cu, slots = mem[:1], mem[4:4 + batch], mem[4 + a:5 + a + batch], mem[4 + a + b:]
-    ws = workspace(dev) if ws is None else ws
-    at = mem.data_ptr()
-    _launch(N.lib().nvfp4_plan_pages, "nvfp4_plan_pages", dev, cached_lens.data_ptr(),
-            new_lens.data_ptr(), batch, block_table.data_ptr(), _row_stride(block_table),
-            max_pages, free_pages.data_ptr(), free_pages.shape[0], free_head.data_ptr(),
-            page_tokens, n_pages, at + 16, at + 16 + 4 * a, at + 16 + 4 * (a + b), max_new, at,
-            ws.data_ptr(), ws.numel())
-    return PagePlan(seq, cu, slots, head)
+    return PagePlan(*(_binding or _load_binding()).plan_pages(
+        cached_lens, new_lens, block_table, free_pages, free_head, page_tokens, n_pages, max_new,
+        ws))
 
 
 class KVCache8:
@@ -360,45 +316,13 @@ class KVCache8:
                  for _ in range(2)]
         return cls(*codes, *scale)
 
-    def c_struct(self) -> N.Kv8Cache:
-        return N.Kv8Cache(self.k_codes.data_ptr(), self.v_codes.data_ptr(),
-                          self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.n_pages,
-                          self.page_tokens, self.kv_heads, self.head_dim)
-
-    def _rows(self, name: str, t: torch.Tensor, heads: int) -> int:
-        """The token stride of a bf16 tensor [tokens, heads, head_dim] or [tokens,
-        heads * head_dim] whose tokens are contiguous."""
-        d = self.head_dim
-        if t.dim() == 3:
-            n, h, e = t.shape
-            stride, sh, se = t.stride()
-            ok = h == heads and e == d and se == 1 and (sh == d or heads == 1)
-        else:
-            n, e = t.shape if t.dim() == 2 else (0, -1)
-            stride = t.stride(0) if t.dim() == 2 else 0
-            ok = e == heads * d and t.stride(1) == 1
-        if not ok or t.dtype is not torch.bfloat16 or t.device != self.k_codes.device:
-            raise ValueError(f"{name} must be a bf16 tensor [tokens, {heads}, {d}] on "
-                             f"{self.k_codes.device}, contiguous inside a token")
-        return stride if n > 1 else heads * d
-
     def append(self, k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
                ws: Optional[torch.Tensor] = None) -> None:
         """nvfp4_kv8_append: writes the tokens of k and v (bf16 [tokens,
         kv_heads, head_dim], views into a fused projection included) to their
         slots (a plan's slot_map; its first entries, if it is longer)."""
-        stride = self._rows("k", k, self.kv_heads)
-        tokens = k.shape[0]
-        if v.shape[0] != tokens or self._rows("v", v, self.kv_heads) != stride:
-            raise ValueError("k and v must share their tokens and a token stride")
-        _check_int32(k.device, "slot_map", slot_map)
-        if slot_map.shape[0] < tokens:
-            raise ValueError(f"slot_map must have at least {tokens} entries")
-        ws = workspace(k.device) if ws is None else ws
-        cs = self.c_struct()
-        _launch(N.lib().nvfp4_kv8_append, "nvfp4_kv8_append", k.device, ctypes.byref(cs),
-                k.data_ptr(), v.data_ptr(), stride, tokens, slot_map.data_ptr(), ws.data_ptr(),
-                ws.numel())
+        (_binding or _load_binding()).kv8_append(self.k_codes, self.v_codes, self.k_scale,
+                                                 self.v_scale, k, v, slot_map, ws)
 
     def attention(self, q: torch.Tensor, cu_q: torch.Tensor, seq_lens: torch.Tensor,
                   block_table: torch.Tensor, max_q: Optional[int] = None,
@@ -419,41 +343,9 @@ class KVCache8:
         Returns out [tokens, q_heads, head_dim] in bf16, and with return_lse the
         fp32 log-sum-exp [tokens, q_heads] too.  Rows of no request are left as
         they are in `out`."""
-        if q.dim() != 3 or q.shape[2] != self.head_dim:
-            raise ValueError(f"q must be [tokens, q_heads, {self.head_dim}]")
-        tokens, heads = q.shape[0], q.shape[1]
-        stride = self._rows("q", q, heads)
-        dev = q.device
-        _check_int32(dev, "cu_q", cu_q)
-        _check_int32(dev, "seq_lens", seq_lens)
-        _check_int32(dev, "block_table", block_table, 2)
-        batch, pages = block_table.shape
-        if cu_q.shape[0] != batch + 1 or seq_lens.shape[0] != batch:
-            raise ValueError("attention: cu_q must be [batch + 1], seq_lens [batch] and "
-                             "block_table [batch, pages]")
-        if out is None:
-            out = torch.empty((tokens, heads, self.head_dim), dtype=torch.bfloat16, device=dev)
-            out_stride = heads * self.head_dim
-        elif out.shape != q.shape:
-            raise ValueError("out must have q's shape")
-        else:
-            out_stride = self._rows("out", out, heads)
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev) if return_lse else None
-        cs = self.c_struct()
-        cb = N.Kv8Batch(cu_q.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(),
-                        _row_stride(block_table), batch, pages,
-                        max(tokens, 1) if max_q is None else max_q,
-                        pages * self.page_tokens if max_kv is None else max_kv)
-        ws = workspace(dev) if ws is None else ws
-        need = int(N.lib().nvfp4_kv8_attention_scratch_bytes(
-            ctypes.byref(cs), ctypes.byref(cb), tokens, heads, int(causal)))
-        # a tensor of the call's own: calls on other streams and captured graphs share nothing
-        scratch = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        _launch(N.lib().nvfp4_kv8_attention, "nvfp4_kv8_attention", dev, ctypes.byref(cs),
-                ctypes.byref(cb), q.data_ptr(), stride, tokens, heads, int(causal),
-                self.head_dim ** -0.5 if scale is None else float(scale), out.data_ptr(),
-                out_stride, _ptr(lse), _ptr(scratch), need, ws.data_ptr(), ws.numel())
-        return (out, lse) if return_lse else out
+        return (_binding or _load_binding()).kv8_attention(
+            self.k_codes, self.v_codes, self.k_scale, self.v_scale, q, cu_q, seq_lens,
+            block_table, max_q, max_kv, causal, scale, out, return_lse, ws)
 
 
 class SinkPlan:

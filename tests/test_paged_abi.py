@@ -218,3 +218,33 @@ def test_binding_refuses_before_the_library():
     for bad in (dict(x=x.half()), dict(x=x, out=torch.zeros(2, 8).half())):
         with pytest.raises(TypeError):
             nv.gemv(w=w, **bad)
+
+
+def test_compiled_binding_refuses():
+    """What only the compiled binding sees: wrong kinds of argument, numbers that do not fit."""
+    c = _cpu_cache()
+    i = torch.zeros(2, dtype=torch.int32)
+    good = dict(q=torch.zeros(3, 4, 64, dtype=torch.bfloat16), cu_q=torch.zeros(3).int(),
+                seq_lens=i, block_table=i.view(2, 1))
+    for bad in (dict(q=None), dict(cu_q=[0, 1, 2]), dict(max_q=1.5), dict(max_kv="1"),
+                dict(scale="1"), dict(out=1)):
+        with pytest.raises(TypeError):
+            c.attention(**{**good, **bad})
+    for bad in (dict(max_q=2 ** 31), dict(max_kv=-2 ** 31 - 1)):
+        with pytest.raises(ValueError):
+            c.attention(**{**good, **bad})
+    with pytest.raises(OverflowError):
+        c.attention(**good, max_q=2 ** 64)
+    with pytest.raises(TypeError):
+        c.append(None, None, i)
+    for bad, error in ((dict(max_new=2 ** 31), ValueError), (dict(max_new=-1), ValueError),
+                       (dict(max_new=None), TypeError)):
+        with pytest.raises(error):
+            nv.plan_pages(i, i, i.view(2, 1), i, i[:1], **{**dict(page_tokens=16, n_pages=4,
+                                                                 max_new=3), **bad})
+    with pytest.raises(ValueError, match="CUDA"):
+        c.attention(**good)
+    # a cache whose buffers were exchanged is looked at again
+    c.k_codes = c.k_codes[:2]
+    with pytest.raises(ValueError):
+        c.append(torch.zeros(2, 2, 64).bfloat16(), torch.zeros(2, 2, 64).bfloat16(), i)
