@@ -194,6 +194,8 @@ namespace append {
 
 constexpr int kThreads = 128;
 constexpr int kHeld = 8;  // rows of a thread kept in registers between the two passes
+constexpr int kMaxCluster = 8;
+constexpr int kResident = 5;  // CTAs of an SM: six (80 registers) spill
 
 struct Args {
   const uint16_t* x[2];    // K, V: bf16, token t, head h at t * stride + h * dim
@@ -201,9 +203,10 @@ struct Args {
   uint8_t* codes[2];       // [page][head][token][dim]
   float* scale[2];         // [page][head]
   const int32_t* slots;    // [tokens]
-  int32_t tokens, heads, page_tokens, per_cta;
+  int32_t tokens, heads, page_tokens, per_tile;
+  int32_t parts, per_part;  // of a tile's 2 * heads heads of K and V
   int64_t n_slots;         // n_pages * page_tokens
-  FastDiv page_div;
+  FastDiv page_div, part_div;
   uint32_t* status;
 };
 
@@ -217,34 +220,44 @@ __device__ __forceinline__ int fit_exponent(uint32_t bits) {
   return max(NVFP4_KV8_MIN_EXP, min(NVFP4_KV8_MAX_EXP, e));
 }
 
-// Largest magnitude of 8 bf16 values as bf16 bits, non-finite ones left out.
-__device__ __forceinline__ uint32_t amax8(uint4 v, bool& nonfinite) {
-  uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
-                        __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-  m = max(m & 0xFFFFu, m >> 16);
-  if (m >= 0x7F80u) {
-    nonfinite = true;
-    m = 0;
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t b = (w[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
-      if (b < 0x7F80u) m = max(m, b);
-    }
-  }
-  return m;
+// The larger of m and the magnitudes of 8 bf16 values, as bf16 bits, in each half.
+__device__ __forceinline__ uint32_t amax8(uint4 v, uint32_t m) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(m, __vmaxu2(v.x & kAbs, v.y & kAbs)),
+                  __vmaxu2(v.z & kAbs, v.w & kAbs));
 }
 
-// 8 bf16 values times inv -> 8 E4M3 bytes (nearest even, saturating; NaN -> 0).
-__device__ __forceinline__ uint2 encode8(uint4 v, float inv) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t h[4];
+// 8 bf16 values with the non-finite ones zero.
+__device__ __forceinline__ uint4 finite8(uint4 v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xFFFF0000u) * inv;
-    lo = lo == lo ? lo : 0.0f;
-    hi = hi == hi ? hi : 0.0f;
-    h[i] = e4m3x2(hi, lo);
+    if ((w[i] & 0x7F80u) == 0x7F80u) w[i] &= 0xFFFF0000u;
+    if ((w[i] & 0x7F800000u) == 0x7F800000u) w[i] &= 0xFFFFu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 bf16 values with the NaN zero.
+__device__ __forceinline__ uint4 no_nan8(uint4 v) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7FFFu) > 0x7F80u) w[i] &= 0xFFFF0000u;
+    if ((w[i] & 0x7FFFFFFFu) > 0x7F80FFFFu) w[i] &= 0xFFFFu;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 bf16 values (none a NaN) times inv, a power of two twice in bf16 -> 8 E4M3 bytes
+// (nearest even, saturating).  The product is exact, or so small (bf16 subnormal) that its
+// code is zero either way: one rounding.
+__device__ __forceinline__ uint2 encode8(uint4 v, uint32_t inv) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w}, h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(inv));
+    h[i] = e4m3x2(__uint_as_float(w[i] & 0xFFFF0000u), __uint_as_float(w[i] << 16));
   }
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
@@ -258,93 +271,221 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   return h[0] | (h[1] << 16);
 }
 
-// Largest value over the CTA.
+// Largest value over the CTA.  The callers alternate between two buffers: one barrier.
 __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* buf) {
   v = __reduce_max_sync(0xFFFFFFFFu, v);
-  __syncthreads();
   if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
   return max(max(buf[0], buf[1]), max(buf[2], buf[3]));
 }
 
-// One CTA takes the runs (tokens in a row whose slots follow one another inside a
-// page) that begin among its per_cta tokens, for one head and one of K and V: the
-// scale of a page is set by one CTA, which sees all of the page's new tokens.
-// HBM-bound when there are many tokens (4 bytes read and 2 written for each K and
-// V element pair): a run is read once, up to kHeld rows a thread in registers.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Largest value over a cluster of n CTAs; buf is this CTA's, 4 words for each rank.
+__device__ __forceinline__ uint32_t cluster_max(uint32_t v, uint32_t* buf, uint32_t rank, int n) {
+  v = __reduce_max_sync(0xFFFFFFFFu, v);
+  const int lane = threadIdx.x & 31;
+  if (lane < n) {
+    const uint32_t own = static_cast<uint32_t>(
+        __cvta_generic_to_shared(buf + 4 * rank + (threadIdx.x >> 5)));
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(own), "r"(lane));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+  }
+  cluster_arrive();
+  cluster_wait();
+  return __reduce_max_sync(0xFFFFFFFFu, lane < 4 * n ? buf[lane] : 0);
+}
+
+// A run is a row of tokens whose slots follow one another inside a page; the scale of a
+// page is set by whoever has its run, from all of the run's tokens.  A tile of per_tile
+// tokens belongs to one CTA, or where pages are longer than a CTA holds in registers
+// (kHeld rows a thread) to a cluster, for per_part of the heads of K and V: it takes the
+// runs that begin in the tile, one head after another.  A run that a warp holds is a
+// warp's, the warps taking turns; one that a CTA holds a CTA's; a longer one is divided
+// among the cluster, and its largest value found over distributed shared memory.
+//
+// HBM-bound when there are many tokens (2 bytes read and 1 written per element).  A chunk
+// of slots is read at once and gives the beginnings and lengths of all its runs, for all
+// heads of the part, so that each head's rows are one load latency and are read once.
+//
+// 18 thousand tokens of 8 heads of 128 in 64-token pages (113 MB): 26 us, 66% of the copy rate
+// (one head a CTA 30 us: the latency of the slots in front of every 16 KB; 16-token pages of
+// 64 elements 21 us).  512 single tokens 11 us, 33 of them 3.4 us: two load latencies and
+// the launch.  Pages of 880 tokens 69 us, 115 without the clusters.
 template <int kDim>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Args a) {
-  constexpr int kLanes = kDim / 8;              // threads of a token row
-  constexpr int kRows = kThreads / kLanes;      // token rows of a pass
-  __shared__ uint32_t buf[kThreads / 32];
-  const int tid = threadIdx.x, u = tid % kLanes, row = tid / kLanes;
-  const int h = blockIdx.y, plane = blockIdx.z;
+__global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Args a) {
+  constexpr int kLanes = kDim / 8;  // threads of a token row
+  constexpr int kWarps = kThreads / 32;
+  static_assert(kWarps == 4, "cta_max and cluster_max");
+  __shared__ uint32_t begins[kWarps], stops[kWarps], shorts[kWarps];
+  __shared__ int32_t slot_of[kThreads], len_of[kThreads];
+  __shared__ uint32_t own_buf[2][kWarps], all_buf[2][kWarps * kMaxCluster];
+  const int tid = threadIdx.x, u = tid % kLanes;
   const int page_tokens = a.page_tokens;
+  uint32_t rank, ranks;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  // the parts of a tile next to one another: CTAs that run together read whole rows of x
+  const uint32_t cta = blockIdx.x / ranks, tile = fast_div(a.part_div, cta);
+  const int item0 = int(cta - tile * uint32_t(a.parts)) * a.per_part;
+  const int item_end = min(item0 + a.per_part, 2 * a.heads);
+  if (ranks > 1) cluster_arrive();  // waited for before the first store to another CTA
+  bool started = ranks == 1;
   pdl_wait();
   pdl_trigger();
-  const uint16_t* x = a.x[plane] + int64_t(h) * kDim + 8 * u;
-  const int t_end = min(a.tokens, (int(blockIdx.x) + 1) * a.per_cta);
+  const int t0 = int(tile) * a.per_tile;
+  const int t_end = min(a.tokens, t0 + a.per_tile);
   bool nonfinite = false;
-  for (int t = int(blockIdx.x) * a.per_cta; t < t_end;) {
-    const int64_t s = a.slots[t];
-    if (s < 0 || s >= a.n_slots) {
-      if (s != -1 && tid == 0) record_status(a.status, NVFP4_ERR_INVALID_ARG);
-      ++t;
-      continue;
-    }
+  uint32_t warp_turn = 0, cta_turn = 0, own_uses = 0, all_uses = 0;
+
+  // the run of len tokens from token t at slot s, by `set` threads (a warp, a CTA or the
+  // cluster) of which this is `id`
+  auto take = [&](int t, int s, int len, int id, int set) {
     const int page = int(fast_div(a.page_div, uint32_t(s)));
-    const int off = int(s) - page * page_tokens;
-    // length of the run: the first place where the slots do not go on
-    const int most = min(page_tokens - off, a.tokens - t);
-    uint32_t stop = 0;  // most - index of the break, so that the largest is the first
-    for (int i = 1 + tid; i < most && stop == 0; i += kThreads)
-      if (a.slots[t + i] != int(s) + i) stop = uint32_t(most - i);
-    const int len = most > 1 ? most - int(cta_max(stop, buf)) : 1;
-    if (off > 0 && t > 0 && t == int(blockIdx.x) * a.per_cta && a.slots[t - 1] == int(s) - 1) {
-      t += len;  // the rest of a run that the previous CTA has
-      continue;
-    }
-    const uint16_t* src = x + int64_t(t) * a.stride;
-    const int64_t ph = int64_t(page) * a.heads + h;
-    uint8_t* dst = a.codes[plane] + ph * page_tokens * kDim;
-    float* scale = a.scale[plane] + ph;
-    const float was = off > 0 ? *scale : 0.0f;
-    uint4 v[kHeld];
-    uint32_t top = 0;
+    const int off = s - page * page_tokens;
+    const int r0 = id / kLanes, step = set / kLanes;
+    for (int item = item0; item < item_end; ++item) {
+      const bool is_v = item >= a.heads;
+      const int h = is_v ? item - a.heads : item;
+      const uint16_t* src = (is_v ? a.x[1] : a.x[0]) + int64_t(t) * a.stride + h * kDim + 8 * u;
+      const int64_t ph = int64_t(page) * a.heads + h;
+      uint8_t* dst = (is_v ? a.codes[1] : a.codes[0]) + ph * page_tokens * kDim;
+      float* scale = (is_v ? a.scale[1] : a.scale[0]) + ph;
+      const float was = off > 0 ? *scale : 0.0f;
+      uint4 v[kHeld];
+      const uint16_t* in = src + r0 * a.stride;
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const int i = row + j * kRows;
-      v[j] = i < len ? ld_nc_v4(src + i * a.stride) : make_uint4(0, 0, 0, 0);
-    }
+      for (int j = 0; j < kHeld; ++j, in += step * a.stride)
+        v[j] = r0 + j * step < len ? ld_nc_v4(in) : make_uint4(0, 0, 0, 0);
+      uint32_t tops = 0;  // even and odd elements
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) top = max(top, amax8(v[j], nonfinite));
-    for (int i = row + kHeld * kRows; i < len; i += kRows)
-      top = max(top, amax8(ld_nc_v4_l1(src + i * a.stride), nonfinite));
-    const float fit = pow2(fit_exponent(cta_max(top, buf)));
-    const float now = fmaxf(was, fit);
-    const float inv = 1.0f / now;
+      for (int j = 0; j < kHeld; ++j) tops = amax8(v[j], tops);
+      for (int i = r0 + kHeld * step; i < len; i += step, in += step * a.stride)
+        tops = amax8(ld_nc_v4_l1(in), tops);
+      uint32_t top = max(tops & 0xFFFFu, tops >> 16);
+      const bool odd = top >= 0x7F80u;  // the thread's part has infinities or NaN
+      if (odd) {
+        nonfinite = true;
+        tops = 0;
+        for (int i = r0; i < len; i += step)
+          tops = amax8(finite8(ld_nc_v4_l1(src + i * a.stride)), tops);
+        top = max(tops & 0xFFFFu, tops >> 16);
 #pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-      const int i = row + j * kRows;
-      if (i < len) *reinterpret_cast<uint2*>(dst + (off + i) * kDim + 8 * u) = encode8(v[j], inv);
+        for (int j = 0; j < kHeld; ++j) v[j] = no_nan8(v[j]);
+      }
+      if (set == 32) {
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+      } else if (set == kThreads) {
+        top = cta_max(top, own_buf[own_uses++ & 1]);
+      } else {
+        if (!started) cluster_wait();
+        started = true;
+        top = cluster_max(top, all_buf[all_uses++ & 1], rank, int(ranks));
+      }
+      const float now = fmaxf(was, pow2(fit_exponent(top)));
+      const uint32_t inv = 0x7F00u - (__float_as_uint(now) >> 16);  // 1 / now in bf16
+      const uint32_t inv2 = inv | (inv << 16);
+      uint8_t* const to = dst + (off + r0) * kDim + 8 * u;
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) {
+        const uint2 c = encode8(v[j], inv2);
+        if (r0 + j * step < len) *reinterpret_cast<uint2*>(to + j * step * kDim) = c;
+      }
+      for (int i = r0 + kHeld * step; i < len; i += step) {
+        uint4 x8 = ld_nc_v4_l1(src + i * a.stride);
+        if (odd) x8 = no_nan8(x8);
+        *reinterpret_cast<uint2*>(dst + (off + i) * kDim + 8 * u) = encode8(x8, inv2);
+      }
+      if (off > 0 && now > was) {
+        const float ratio = was * __uint_as_float(inv << 16);
+        for (int i = id; i < off * kDim / 16; i += set) {
+          uint4 q = reinterpret_cast<uint4*>(dst)[i];
+          q.x = recode4(q.x, ratio);
+          q.y = recode4(q.y, ratio);
+          q.z = recode4(q.z, ratio);
+          q.w = recode4(q.w, ratio);
+          reinterpret_cast<uint4*>(dst)[i] = q;
+        }
+      }
+      if (id == 0) *scale = now;
     }
-    for (int i = row + kHeld * kRows; i < len; i += kRows)
-      *reinterpret_cast<uint2*>(dst + (off + i) * kDim + 8 * u) =
-          encode8(ld_nc_v4_l1(src + i * a.stride), inv);
-    if (off > 0 && now > was) {
-      const float ratio = was * inv;
-      for (int i = tid; i < off * kDim / 16; i += kThreads) {
-        uint4 w = reinterpret_cast<uint4*>(dst)[i];
-        w.x = recode4(w.x, ratio);
-        w.y = recode4(w.y, ratio);
-        w.z = recode4(w.z, ratio);
-        w.w = recode4(w.w, ratio);
-        reinterpret_cast<uint4*>(dst)[i] = w;
+  };
+
+  for (int base = t0; base < t_end; base += kThreads) {
+    if (base != t0) __syncthreads();
+    const int mine = base + tid;
+    bool begin = false, stop = true;  // of a run; not the continuation of one
+    int most = 0;                     // tokens of a run that begins here, by page and tokens
+    if (mine < a.tokens) {
+      const int32_t s = a.slots[mine], before = mine > 0 ? a.slots[mine - 1] : -1;
+      slot_of[tid] = s;
+      if (s >= 0 && s < a.n_slots) {
+        const int off = s - int(fast_div(a.page_div, uint32_t(s))) * page_tokens;
+        stop = off == 0 || before != s - 1;
+        begin = stop && mine < t_end;
+        most = min(page_tokens - off, a.tokens - mine);
+      } else if (s != -1 && mine < t_end) {
+        record_status(a.status, NVFP4_ERR_INVALID_ARG);
       }
     }
-    if (tid == 0) *scale = now;
-    t += len;
+    const uint32_t bw = __ballot_sync(0xFFFFFFFFu, begin), sw = __ballot_sync(0xFFFFFFFFu, stop);
+    if ((tid & 31) == 0) {
+      begins[tid >> 5] = bw;
+      stops[tid >> 5] = sw;
+    }
+    __syncthreads();
+    int len = kThreads - tid;  // to the next stop, or to the chunk's end and maybe on (open)
+    bool open = true;
+#pragma unroll
+    for (int w = kWarps - 1; w >= 0; --w) {
+      const uint32_t later = w < (tid >> 5)   ? 0
+                             : w > (tid >> 5) ? stops[w]
+                                              : stops[w] & (0xFFFFFFFEu << (tid & 31));
+      if (later) {
+        len = 32 * w + __ffs(later) - 1 - tid;
+        open = false;
+      }
+    }
+    open = open && len < most;
+    len_of[tid] = open ? -len : len;
+    const uint32_t few = __ballot_sync(0xFFFFFFFFu, begin && !open && len <= kHeld * 32 / kLanes);
+    if ((tid & 31) == 0) shorts[tid >> 5] = few;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      for (uint32_t bits = begins[w] & ~shorts[w]; bits != 0; bits &= bits - 1) {
+        const int at = 32 * w + __ffs(bits) - 1, t = base + at, s = slot_of[at];
+        int n = len_of[at];
+        if (n < 0) {
+          // most - the place of the break behind the chunk, the largest the first
+          const int off = s - int(fast_div(a.page_div, uint32_t(s))) * page_tokens;
+          const int limit = min(page_tokens - off, a.tokens - t);
+          uint32_t left = 0;
+          for (int i = tid - n; i < limit && left == 0; i += kThreads)
+            if (a.slots[t + i] != s + i) left = uint32_t(limit - i);
+          n = limit - int(cta_max(left, own_buf[own_uses++ & 1]));
+        }
+        if (n <= kHeld * kThreads / kLanes || ranks == 1) {
+          if ((cta_turn++ & (ranks - 1)) == rank) take(t, s, n, tid, kThreads);
+        } else {
+          take(t, s, n, int(rank) * kThreads + tid, kThreads * int(ranks));
+        }
+      }
+    }
+    const uint32_t warp = rank * kWarps + (tid >> 5);
+    for (int w = 0; w < kWarps; ++w)
+      for (uint32_t bits = shorts[w]; bits != 0; bits &= bits - 1)
+        if ((warp_turn++ & (kWarps * ranks - 1)) == warp) {
+          const int at = 32 * w + __ffs(bits) - 1;
+          take(base + at, slot_of[at], len_of[at], tid & 31, 32);
+        }
   }
+  if (!started) cluster_wait();
   if (nonfinite) record_status(a.status, NVFP4_ERR_DOMAIN);
 }
 
@@ -366,15 +507,34 @@ cudaError_t launch_kv8_append(const LaunchKv8Append& p, cudaStream_t st) {
   a.n_slots = int64_t(p.n_pages) * p.page_tokens;
   a.page_div = make_fastdiv(uint32_t(p.page_tokens));
   a.status = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.ws) + kWsStatus);
-  // few tokens: one a CTA (each may be a run of its own); many: up to a page's worth, so
-  // that CTAs without a run's beginning stay few
-  int64_t per = p.tokens * p.heads * 2 / (int64_t(p.sm_count) * 16);
-  per = per < 1 ? 1 : per > p.page_tokens ? p.page_tokens : per;
-  a.per_cta = int32_t(per);
-  const dim3 grid(unsigned((p.tokens + per - 1) / per), unsigned(p.heads), 2);
+  // as many CTAs as hold a page's rows in registers, if there are that many tokens
+  const int64_t held = append::kHeld * append::kThreads / (p.head_dim / 8);
+  const int64_t longest = p.tokens < p.page_tokens ? p.tokens : p.page_tokens;
+  int64_t ranks = 1;
+  while (ranks < append::kMaxCluster && ranks * held < longest) ranks *= 2;
+  // About 8 CTAs an SM.  Few tokens: short tiles, as every token may be a run of its own;
+  // many: as long as a page or four warps' runs, so that few tiles have no beginning.
+  const int64_t ctas = int64_t(p.sm_count) * 8;
+  const int64_t widest = p.page_tokens > 64 ? p.page_tokens : 64;
+  int64_t per = p.tokens * p.heads * 2 * ranks / ctas;
+  per = per < 1 ? 1 : per > widest ? widest : per;
+  a.per_tile = int32_t(per);
+  // ... and then several heads a CTA, for which the slots are looked at once
+  const int64_t tiles = (p.tokens + per - 1) / per;
+  int64_t part = tiles * p.heads * 2 * ranks / ctas;
+  part = part < 1 ? 1 : part > 2 * p.heads ? 2 * p.heads : part;
+  a.per_part = int32_t(part);
+  a.parts = int32_t((2 * p.heads + part - 1) / part);
+  a.part_div = make_fastdiv(uint32_t(a.parts));
+  const dim3 grid(unsigned(tiles * a.parts * ranks));
+  const dim3 cluster(static_cast<unsigned>(ranks), 1, 1), block(append::kThreads);
+  if (ranks == 1)
+    return p.head_dim == 64
+               ? launch_pdl(append::append_kernel<64>, grid, block, 0, st, a)
+               : launch_pdl(append::append_kernel<128>, grid, block, 0, st, a);
   return p.head_dim == 64
-             ? launch_pdl(append::append_kernel<64>, grid, dim3(append::kThreads), 0, st, a)
-             : launch_pdl(append::append_kernel<128>, grid, dim3(append::kThreads), 0, st, a);
+             ? launch_pdl_cluster(append::append_kernel<64>, grid, cluster, block, 0, st, a)
+             : launch_pdl_cluster(append::append_kernel<128>, grid, cluster, block, 0, st, a);
 }
 
 }  // namespace nvfp4

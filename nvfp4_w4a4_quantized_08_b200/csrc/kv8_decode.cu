@@ -366,9 +366,9 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
             topv = fmaxf(topv, x + lv[g]);
           }
 #pragma unroll
-          for (int o = 4; o <= 16; o <<= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            topv = fmaxf(topv, __shfl_xor_sync(0xFFFFFFFFu, topv, o));
+          for (int m = 4; m <= 16; m <<= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+            topv = fmaxf(topv, __shfl_xor_sync(0xFFFFFFFFu, topv, m));
           }
           // (-inf stays: such a row has seen nothing)
           const float was = lim[nt][j] - kLazy, wasv = limv[nt][j] - kLazy;

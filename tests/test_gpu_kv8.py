@@ -543,3 +543,27 @@ def test_scores_that_rise_all_along(nq, step):
     want = ref.attention(q.cpu().double(), *_planes64(c), [list(range(64))], [nq], [1024], 16,
                          False, 0.125)
     ref.assert_attention_close(o, lse, want)
+
+
+@pytest.mark.parametrize("heads,dim,page", [(3, 128, 880), (1, 64, 304), (2, 128, 112), (9, 64, 16)])
+def test_append_runs_of_all_lengths(heads, dim, page):
+    """Single tokens between runs that a warp, a CTA and several CTAs hold, skipped tokens
+    among them, more tokens than a tile."""
+    r = random.Random(heads * page)
+    counts = [r.choice((1, 1, 1, 2, 17, 33, 64, 65, 129, 300, 1000)) for _ in range(40)]
+    cached = [r.randint(0, 2 * page) for _ in counts]
+    table, free, n_pages = _tables(cached, counts, page, 2, 3)
+    _, _, slots, _, _ = ref.plan(cached, counts, table, free, 0, page)
+    at = 0
+    for n in counts:   # a padded batch: some requests' last tokens are not stored
+        if n > 1 and r.random() < 0.3:
+            slots[at + n - 1] = -1
+        at += n
+    c = _random_cache(n_pages, page, heads, dim, 4)
+    before = _planes64(c)
+    g = torch.Generator().manual_seed(5)
+    k, v = (torch.randn(sum(counts), heads, dim, generator=g).mul_(torch.exp2(
+        torch.randint(-6, 7, (sum(counts), 1, 1), generator=g).float())) for _ in range(2))
+    k, v = k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda()
+    c.append(k, v, i32(slots))
+    _check_append(c, k, v, slots, before)
