@@ -33,10 +33,13 @@
 // a prologue, cost 0.7 us at 1024 x 1024.)  The 16 weight rows of a product are 4 i-values by
 // 4 rows 32 apart: the scale tile of the tensor-core layout keeps their scales in 64
 // contiguous bytes.  Where rows alone leave SMs idle, a cluster of up to 8 CTAs splits the
-// columns again and joins the sums through distributed shared memory in rank order: no
-// workspace, no atomics, the same result every time.
-#include <cooperative_groups.h>
-
+// columns again; each CTA stores its sums to the one that finishes them, which adds them in
+// rank order: no workspace, no atomics, the same result every time.  (Fetching the others' sums
+// instead took 2 us a CTA of the cluster: 7 x 5000 x 14336 in clusters of 6 37 us against 23.)
+//
+// 1 x 1024 x 1024 2.6 us (the launch, one step, the join of the warps); 1 x 14336 x 4096 11.4 us,
+// 44% of the copy rate; 7 x 5000 x 14336 in fp32 22 us, 29%, the conversions' and products'
+// latency with 16 warps an SM.
 #include <algorithm>
 
 #include "common.cuh"
@@ -129,10 +132,13 @@ constexpr int kRingBytes = std::max(kWarps * kStages * kRowTiles<NT> * 16 * (kSt
 template <bool FP32>
 constexpr int kXBytes = 2 * 16 * (FP32 ? 2 : 1) * kXRow;
 
+// Sums of a cluster's CTAs: KW M <= 16.
+template <int KW, int NT>
+constexpr int kJoinBytes = (kWarps / KW * kRowTiles<NT> * 16 * (16 / KW) + kMaxCluster) * 4;
+
 // KW warps split the columns; NT tiles of 8 product columns; FP32 x in two parts.
 template <int KW, int NT, bool FP32>
 __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
-  namespace cg = cooperative_groups;
   constexpr int kTiles = kRowTiles<NT>;
   constexpr int RG = kWarps / KW;          // groups of 16 kTiles weight rows
   constexpr int kOf128 = 8 / kTiles;       // groups of a 128-row tile
@@ -150,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kw = warp % KW, rg = warp / KW;
   const int r = lane >> 2, c = lane & 3;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int cs = int(cluster.num_blocks()), rank = int(cluster.block_rank());
+  const int cs = int(cluster_size()), rank = int(cluster_rank());
+  if (cs > 1) cluster_arrive();   // waited for before the first store to another CTA
   const int group0 = int(blockIdx.x) / cs * RG;
   const int n_steps = (a.K + kStep - 1) / kStep;
   const int stride = KW * cs;                          // steps between a warp's own
@@ -168,8 +174,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
   };
   // copies: lane l takes 16-byte unit l % 8 of rows l / 8 + 4 i; units exchanged by the row's
   // place, so that the reads below meet no bank twice
-  const int64_t pitch = a.K / 2;
-  const uint8_t* from[kTiles * 4];
+  uint32_t from[kTiles * 4];   // in units of 16 bytes: below 2^30
   uint32_t to[4];
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
                         uint32_t(warp) * kStages * kStage;
@@ -179,19 +184,19 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
     to[i] = ring + rho * 128 + (((lane & 7) ^ (rho & 7)) << 4);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t)
-      from[4 * t + i] = a.codes + row_of(t, rho) * pitch + 16 * (lane & 7);
+      from[4 * t + i] = uint32_t(row_of(t, rho)) * uint32_t(a.K / 32) + (lane & 7);
   }
   auto issue = [&](int i) {   // step i of this warp
     const int st = first + i * stride;
     if (i < iters && st < n_steps) {
       const uint32_t in = st * kStep + 32 * (lane & 7) < a.K ? 16 : 0;
       const uint32_t stage = uint32_t(i % kStages) * kStage;
-      const int64_t at = in ? int64_t(st) * (kStep / 2) : 0;
+      const uint32_t at = in ? uint32_t(st) * (kStep / 32) : 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
-          copy16(to[j] + stage + t * 16 * (kStep / 2), from[4 * t + j] + at, in);
+          copy16(to[j] + stage + t * 16 * (kStep / 2), a.codes + 16 * int64_t(from[4 * t + j] + at), in);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -425,57 +430,104 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
       red[warp][16 * t + r + 8][8 * n + 2 * c] = acc[t][n][2];
       red[warp][16 * t + r + 8][8 * n + 2 * c + 1] = acc[t][n][3];
     }
-  if (cs > 1) cluster.sync(); else __syncthreads();
+  __syncthreads();
   const float st = __ldg(a.s_t);
-  for (int o = rank * kThreads + tid; o < RG * kTiles * 16 * a.M; o += kThreads * cs) {
-    // consecutive threads: the 4 kTiles RG consecutive weight rows of each 32
-    constexpr int kRun = 4 * kTiles * RG;
+  constexpr int kRun = 4 * kTiles * RG;   // consecutive weight rows of each 32
+  auto finish = [&](int o, float sum) {
+    const int i4 = o % kRun, q = (o / kRun) & 3, m = o / (4 * kRun);
+    const int grp = group0 + i4 / (4 * kTiles);
+    const int n = grp / kOf128 * 128 + grp % kOf128 * (4 * kTiles) + i4 % (4 * kTiles) + 32 * q;
+    if (n >= a.N) return;
+    float y = sum * st;
+    if (a.y_bf16) {
+      if (a.act == NVFP4_ACT_GELU_TANH) y = gelu_tanh(__bfloat162float(__float2bfloat16_rn(y)));
+      static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(y);
+    } else {
+      if (a.act == NVFP4_ACT_GELU_TANH) y = gelu_tanh(y);
+      static_cast<float*>(a.y)[m * a.ldy + n] = y;
+    }
+  };
+  // a rank finishes `share` of the outputs; the others store their sums of them to it
+  const int total = RG * kTiles * 16 * a.M;
+  const int share = (total + cs - 1) / cs;
+  float* const joined = reinterpret_cast<float*>(xs + kXBytes<FP32>);   // [cs][share]
+  if (cs > 1) cluster_wait();   // the others have started
+  for (int o = tid; o < total; o += kThreads) {
     const int i4 = o % kRun, q = (o / kRun) & 3, m = o / (4 * kRun);
     const int g = i4 / (4 * kTiles), rho = 16 * ((i4 >> 2) % kTiles) + (i4 & 3) + 4 * q;
-    const int grp = group0 + g;
-    const int n = grp / kOf128 * 128 + grp % kOf128 * (4 * kTiles) + i4 % (4 * kTiles) + 32 * q;
     float sum = 0.0f;
-    for (int k = 0; k < cs; ++k) {
-      const float* base =
-          cs > 1 ? cluster.map_shared_rank(&red[0][0][0], k) : &red[0][0][0];
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-        const float* p = base + ((g * KW + w) * kTiles * 16 + rho) * (kCols + 1) + m * kParts;
-        float v = p[0];
-        if constexpr (FP32) v = fmaf(p[1], 0x1p-11f, v);
-        sum += v;
-      }
+    for (int w = 0; w < KW; ++w) {
+      const float* p = &red[g * KW + w][rho][m * kParts];
+      float v = p[0];
+      if constexpr (FP32) v = fmaf(p[1], 0x1p-11f, v);
+      sum += v;
     }
-    if (n < a.N) {
-      float y = sum * st;
-      if (a.y_bf16) {
-        if (a.act == NVFP4_ACT_GELU_TANH) y = gelu_tanh(__bfloat162float(__float2bfloat16_rn(y)));
-        static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(y);
-      } else {
-        if (a.act == NVFP4_ACT_GELU_TANH) y = gelu_tanh(y);
-        static_cast<float*>(a.y)[m * a.ldy + n] = y;
-      }
+    if (cs == 1) {
+      finish(o, sum);
+    } else {
+      const int owner = o / share;
+      store_cluster(joined + rank * share + (o - owner * share), owner, sum);
     }
   }
-  if (cs > 1) cluster.sync();   // peers read this CTA's shared memory until here
+  if (cs == 1) return;
+  cluster_arrive();
+  cluster_wait();
+  for (int i = tid; i < share && rank * share + i < total; i += kThreads) {
+    float sum = 0.0f;
+    for (int k = 0; k < cs; ++k) sum += joined[k * share + i];
+    finish(rank * share + i, sum);
+  }
+}
+
+template <int KW, int NT>
+int ctas_of(const Args& a) {
+  constexpr int RG = kWarps / KW;
+  const int groups = (a.N + 127) / 128 * (8 / kRowTiles<NT>);
+  return (groups + RG - 1) / RG;
+}
+
+// How many CTAs split the columns, and what that costs in quarters of a step: a CTA's steps,
+// 5/4 as long where SMs have two CTAs, in as many waves as it takes (2 CTAs an SM, of clusters
+// 7/4); the join.  7 x 5000 x 14336, fp32: 73 us in 40 CTAs, 29.5 in 120, 29.3 in 160, 23.1 in
+// 240, 30.4 in 280 (two waves); 16 x 9216 x 5120: 52 in 36, 23.1 in 144, 17.3 in 252, 27 in 288;
+// 1 x 1024 x 12800: 9.5 in 32, 5.1 in 128, 6.5 in 160, 4.6 in 224.
+template <int KW>
+int split_of(int ctas, int n_steps, int sm_count, int& cost) {
+  int best = 1;
+  cost = INT32_MAX;
+  for (int cs = 1; cs <= kMaxCluster; ++cs) {
+    const int64_t n = int64_t(ctas) * cs, room = cs == 1 ? 2 * sm_count : sm_count * 7 / 4;
+    const int64_t waves = (n + room - 1) / room, iters = (n_steps + KW * cs - 1) / (KW * cs);
+    const int64_t c = waves * iters * (n > sm_count ? 5 : 4) + (waves - 1) + (cs > 1);
+    if (c < cost) {
+      cost = int(c);
+      best = cs;
+    }
+  }
+  return best;
 }
 
 template <int KW, int NT, bool FP32>
 cudaError_t launch(const Args& a, int sm_count, cudaStream_t st) {
-  constexpr int RG = kWarps / KW;
-  const int groups = (a.N + 127) / 128 * (8 / kRowTiles<NT>);
-  const int ctas = (groups + RG - 1) / RG;
-  const int n_steps = (a.K + kStep - 1) / kStep;
-  // Split the columns over a cluster while every warp has a step and every CTA an SM of its own
-  // (7 x 5000 x 14336: 31 us in 120 CTAs, 37 in 160 to 240, 67 in 40; 1 x 1024 x 12800: 6.1 us in
-  // 128, 7.3 in 256, 9.7 in 32).
-  int cs = std::min(kMaxCluster, std::max(1, sm_count / ctas));
-  cs = std::min(cs, std::max(1, n_steps / KW));
-  constexpr size_t kSmem = (kRingBytes<NT> + 15) / 16 * 16 + kXBytes<FP32>;
+  const int ctas = ctas_of<KW, NT>(a);
+  int cost;
+  const int cs = split_of<KW>(ctas, (a.K + kStep - 1) / kStep, sm_count, cost);
+  constexpr size_t kSmem = (kRingBytes<NT> + 15) / 16 * 16 + kXBytes<FP32> + kJoinBytes<KW, NT>;
   const cudaError_t e = allow_smem<gemv_kernel<KW, NT, FP32>>(kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(gemv_kernel<KW, NT, FP32>, dim3(unsigned(ctas * cs)),
                             dim3(unsigned(cs)), dim3(kThreads), kSmem, st, a);
+}
+
+// One or two rows: all warps on one group of weight rows, or, where that fills the SMs worse,
+// four (1 x 14336 x 4096: 11.5 us with four against 12.2; 1 x 9216 x 5120 9.9 against 7.8).
+bool all_on_one(const Args& a, int sm_count) {
+  const int n_steps = (a.K + kStep - 1) / kStep;
+  int eight, four;
+  split_of<8>(ctas_of<8, 1>(a), n_steps, sm_count, eight);
+  split_of<4>(ctas_of<4, 1>(a), n_steps, sm_count, four);
+  return eight <= four;
 }
 
 }  // namespace gemv
@@ -496,17 +548,15 @@ cudaError_t launch_gemv(const LaunchGemv& g, cudaStream_t st) {
   a.y_bf16 = g.y_dtype == NVFP4_BF16;
   a.act = g.act;
   a.m_div = make_fastdiv(uint32_t(a.M));
-  // KW M <= 16 row-steps are converted at a time; 8 NT >= product columns.  One or two rows over
-  // more weights than two CTAs an SM take with all warps on one group: 64 rows a CTA (1 x 14336 x
-  // 4096: 11.5 us against 12.2; 1 x 9216 x 5120, which fits, 9.9 against 7.8).
-  const bool many = (g.N + 31) / 32 > 2 * g.sm_count;
+  // KW M <= 16 row-steps are converted at a time; 8 NT >= product columns
+  const bool one = g.M <= 2 && gemv::all_on_one(a, g.sm_count);
   if (g.x_dtype == NVFP4_BF16) {
-    if (g.M <= 2 && !many) return gemv::launch<8, 1, false>(a, g.sm_count, st);
+    if (one) return gemv::launch<8, 1, false>(a, g.sm_count, st);
     if (g.M <= 4) return gemv::launch<4, 1, false>(a, g.sm_count, st);
     if (g.M <= 8) return gemv::launch<2, 1, false>(a, g.sm_count, st);
     return gemv::launch<1, 2, false>(a, g.sm_count, st);
   }
-  if (g.M <= 2 && !many) return gemv::launch<8, 1, true>(a, g.sm_count, st);
+  if (one) return gemv::launch<8, 1, true>(a, g.sm_count, st);
   if (g.M <= 4) return gemv::launch<4, 1, true>(a, g.sm_count, st);
   if (g.M <= 8) return gemv::launch<2, 2, true>(a, g.sm_count, st);
   return gemv::launch<1, 4, true>(a, g.sm_count, st);

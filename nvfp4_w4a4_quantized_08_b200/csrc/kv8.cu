@@ -279,24 +279,11 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* buf) {
   return max(max(buf[0], buf[1]), max(buf[2], buf[3]));
 }
 
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Largest value over a cluster of n CTAs; buf is this CTA's, 4 words for each rank.
 __device__ __forceinline__ uint32_t cluster_max(uint32_t v, uint32_t* buf, uint32_t rank, int n) {
   v = __reduce_max_sync(0xFFFFFFFFu, v);
   const int lane = threadIdx.x & 31;
-  if (lane < n) {
-    const uint32_t own = static_cast<uint32_t>(
-        __cvta_generic_to_shared(buf + 4 * rank + (threadIdx.x >> 5)));
-    uint32_t at;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(own), "r"(lane));
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-  }
+  if (lane < n) store_cluster(buf + 4 * rank + (threadIdx.x >> 5), lane, v);
   cluster_arrive();
   cluster_wait();
   return __reduce_max_sync(0xFFFFFFFFu, lane < 4 * n ? buf[lane] : 0);
@@ -328,9 +315,7 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Args 
   __shared__ uint32_t own_buf[2][kWarps], all_buf[2][kWarps * kMaxCluster];
   const int tid = threadIdx.x, u = tid % kLanes;
   const int page_tokens = a.page_tokens;
-  uint32_t rank, ranks;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
   // the parts of a tile next to one another: CTAs that run together read whole rows of x
   const uint32_t cta = blockIdx.x / ranks, tile = fast_div(a.part_div, cta);
   const int item0 = int(cta - tile * uint32_t(a.parts)) * a.per_part;
