@@ -189,16 +189,25 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// v to rank's copy of the shared variable p points to in this CTA.
-template <typename T>
-__device__ __forceinline__ void store_cluster(T* p, uint32_t rank, T v) {
-  static_assert(sizeof(T) == 4, "one word");
-  uint32_t at, w;
-  memcpy(&w, &v, 4);
+// The address of rank's copy of the shared variable p points to in this CTA, and stores there.
+__device__ __forceinline__ uint32_t map_cluster(const void* p, uint32_t rank) {
+  uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                : "=r"(at)
                : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+  return at;
+}
+__device__ __forceinline__ void store_cluster(uint32_t* p, uint32_t rank, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_cluster(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void store_cluster(float* p, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_cluster(p, rank)), "f"(v) : "memory");
+}
+__device__ __forceinline__ void store_cluster4(float* p, uint32_t rank, float x, float y, float z,
+                                               float w) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(map_cluster(p, rank)),
+               "f"(x), "f"(y), "f"(z), "f"(w)
+               : "memory");
 }
 
 // 32-byte store (sm_100 256-bit access); p must be 32-byte aligned.

@@ -8,7 +8,7 @@
 // 8 NT rows).  One CTA takes one tile of rows, one KV head and one range of tokens;
 // its four warps take groups of 16 tokens in turn (2 KB of K and 2 KB of V for 128
 // dims), each through a ring of its own in shared memory that asynchronous 16-byte
-// copies fill kStages - 1 groups ahead: ~144 KB in flight an SM, where the latency of
+// copies fill kStages - 1 groups ahead: ~128 KB in flight an SM, where the latency of
 // HBM at full rate needs ~40 KB and two groups a warp in registers gave 48 KB in
 // theory and 62% of the rate.  Rings are private to a warp, so no barrier is waited on.
 //
@@ -34,16 +34,14 @@
 //
 // Ranges: with few requests and heads the tokens are split over CTAs; each leaves its
 // normalised rows in fp32 and their log-sum-exp, and a second kernel joins them in
-// order of the range, so results do not depend on timing.
+// order of the range, so results do not depend on timing.  Up to 8 ranges of one wave are
+// a cluster, whose CTAs store their rows to the one that joins them (fetching them from one
+// another instead: 0.6 us longer for 777 tokens).
 #include <algorithm>
-
-#include <cooperative_groups.h>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "kv8_batch.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace nvfp4 {
 namespace kv8 {
@@ -123,6 +121,12 @@ __device__ __forceinline__ uint32_t place(uint32_t token, uint32_t unit) {
 template <int kDim, int NT>
 constexpr int kGroups = kDim == 64 && NT == 1 ? 2 : 1;
 
+// Shared memory of a CTA by itself: the rings, or after them the warps' rows.
+template <int kDim, int NT>
+constexpr size_t kOwnBytes =
+    std::max(size_t(kWarps) * kStages * kGroups<kDim, NT> * 2 * 16 * kDim,
+             size_t(kWarps) * 8 * NT * (kDim + 4) * sizeof(float));
+
 // CTAs of an SM: by registers.
 template <int NT>
 constexpr int kResident = NT == 1 ? 4 : 3;
@@ -154,6 +158,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
     const int tok = group_token(n0 + lane);
     return tok < a.max_tokens ? __ldg(table + fast_div(a.page_div, uint32_t(tok))) : 0;
   };
+  if (a.cluster) cluster_arrive();   // waited for before the first store to another CTA
   pdl_wait();
   pdl_trigger();
   const int first_page = load_pages(0);
@@ -164,8 +169,9 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
   const int used = splits_of(a, rq.kv);
   if (rho0 >= rows || split >= used) {
     if (a.cluster) {  // the other CTAs count this one at both barriers
-      cg::this_cluster().sync();
-      cg::this_cluster().sync();
+      cluster_wait();
+      cluster_arrive();
+      cluster_wait();
     }
     return;
   }
@@ -489,8 +495,12 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
     }
   __syncthreads();
   constexpr int kPer = kDim / 16;   // 16 lanes a row
-  // a cluster's parts, behind the warps' rows
-  float (*part)[kDim + 4] = reinterpret_cast<float (*)[kDim + 4]>(&so[kWarps][0][0]);
+  // a cluster's rows of ranges: row `row` is joined by the CTA of range row % used; behind what
+  // a CTA that is not as far still reads
+  float (*joined)[kDim + 4] =
+      reinterpret_cast<float (*)[kDim + 4]>(ring + kOwnBytes<kDim, NT>);
+  const int share = (kRows + used - 1) / used;
+  if (a.cluster) cluster_wait();   // the others have started
   const int d0 = (tid & 15) * kPer;
   for (int row = tid >> 4; row < kRows; row += kThreads / 16) {
     const int rho = rho0 + row;
@@ -521,17 +531,19 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
       v[i] = x * norm;
     }
     if (used > 1 && a.cluster) {
+      float* const to = &joined[split * share + row / used][0];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) part[row][d0 + i] = v[i];
-      if (d0 == 0) part[row][kDim] = lse2;
+      for (int i = 0; i < kPer; i += 4)
+        store_cluster4(to + d0 + i, row % used, v[i], v[i + 1], v[i + 2], v[i + 3]);
+      if (d0 == 0) store_cluster(to + kDim, row % used, lse2);
     } else {
       store_row<kPer, kDim>(a, rq, h, rho, split, used, d0, v, lse2, d0 == 0);
     }
   }
   if (!a.cluster) return;
-  // the ranges of a cluster: row by row through distributed shared memory, in order
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
+  // the ranges of a cluster, in order
+  cluster_arrive();
+  cluster_wait();
   if (used > 1) {
     for (int row = split + (tid >> 4) * used; row < kRows && rho0 + row < rows;
          row += kThreads / 16 * used) {
@@ -541,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
       for (int s = 0; s < kMaxCluster; ++s) {
         lse[s] = kNegInf;
         if (s < used) {
-          from[s] = cluster.map_shared_rank(part[row], s);
+          from[s] = joined[s * share + row / used];
           lse[s] = from[s][kDim];
           top = fmaxf(top, lse[s]);
         }
@@ -571,7 +583,6 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
                             sum == 0.0f ? kNegInf : base + log2f(sum), d0 == 0);
     }
   }
-  cluster.sync();   // the others read this CTA's part until here
 }
 
 // Joins the ranges of requests that were split.  WPR warps a row take its ranges in turn,
@@ -654,15 +665,15 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Args a) {
 
 template <int kDim, int NT>
 cudaError_t launch_decode(const Args& a, dim3 grid, cudaStream_t st) {
-  // the rings, or the joined rows if they are larger
-  constexpr size_t kRing = size_t(kWarps) * kStages * kGroups<kDim, NT> * 2 * 16 * kDim;
-  constexpr size_t kSmem =
-      std::max(kRing, size_t(kWarps + 1) * 8 * NT * (kDim + 4) * sizeof(float));
+  constexpr size_t kOwn = kOwnBytes<kDim, NT>;
+  constexpr size_t kJoin = size_t(8 * NT + kMaxCluster) * (kDim + 4) * sizeof(float);
+  constexpr size_t kForThree = size_t(72) << 10;
+  static_assert(kOwn + kJoin <= kForThree, "a cluster's rows");
   // Clusters get shared memory for three CTAs an SM, as the number of ranges assumes: where a
   // fourth fits, they are packed onto some SMs and leave others idle (16 x 8500 tokens, 4
   // heads: 34 us against 30).
-  const size_t smem = a.cluster ? std::max(kSmem, size_t(72) << 10) : kSmem;
-  const cudaError_t e = allow_smem<decode_kernel<kDim, NT>>(std::max(kSmem, size_t(72) << 10));
+  const size_t smem = a.cluster ? kForThree : kOwn;
+  const cudaError_t e = allow_smem<decode_kernel<kDim, NT>>(std::max(kOwn, kForThree));
   if (e != cudaSuccess) return e;
   return launch_pdl_cluster(decode_kernel<kDim, NT>, grid, dim3(1, 1, a.cluster ? a.n_splits : 1),
                             dim3(kThreads), smem, st, a);
