@@ -194,6 +194,7 @@ namespace append {
 
 constexpr int kThreads = 128;
 constexpr int kHeld = 8;  // rows of a thread kept in registers between the two passes
+constexpr int kOld = 4;   // 16-byte loads of a thread in flight while it codes old tokens again
 constexpr int kMaxCluster = 8;
 constexpr int kResident = 5;  // CTAs of an SM: six (80 registers) spill
 
@@ -269,6 +270,21 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float ratio) {
   for (int i = 0; i < 2; ++i)
     h[i] = e4m3x2(e4m3_to_f32(w >> (16 * i + 8)) * ratio, e4m3_to_f32(w >> (16 * i)) * ratio);
   return h[0] | (h[1] << 16);
+}
+
+// n times 16 old codes, by `set` threads of which this is `id`.  Not inlined: the loads in
+// flight would cost the caller the registers of its rows.
+__device__ __noinline__ void recode(uint4* old, int n, float ratio, int id, int set) {
+  for (int i = id; i < n; i += kOld * set) {
+    uint4 q[kOld];
+#pragma unroll
+    for (int j = 0; j < kOld; ++j) q[j] = old[min(i + j * set, n - 1)];
+#pragma unroll
+    for (int j = 0; j < kOld; ++j)
+      if (i + j * set < n)
+        old[i + j * set] = make_uint4(recode4(q[j].x, ratio), recode4(q[j].y, ratio),
+                                      recode4(q[j].z, ratio), recode4(q[j].w, ratio));
+  }
 }
 
 // Largest value over the CTA.  The callers alternate between two buffers: one barrier.
@@ -389,14 +405,7 @@ __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Args 
       }
       if (off > 0 && now > was) {
         const float ratio = was * __uint_as_float(inv << 16);
-        for (int i = id; i < off * kDim / 16; i += set) {
-          uint4 q = reinterpret_cast<uint4*>(dst)[i];
-          q.x = recode4(q.x, ratio);
-          q.y = recode4(q.y, ratio);
-          q.z = recode4(q.z, ratio);
-          q.w = recode4(q.w, ratio);
-          reinterpret_cast<uint4*>(dst)[i] = q;
-        }
+        recode(reinterpret_cast<uint4*>(dst), off * kDim / 16, ratio, id, set);
       }
       if (id == 0) *scale = now;
     }
