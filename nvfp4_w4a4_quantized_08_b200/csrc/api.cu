@@ -559,6 +559,7 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
     return NVFP4_ERR_MISALIGNED;
   if (!ws || ws_bytes < kWsBytes) return NVFP4_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return NVFP4_ERR_MISALIGNED;
+  if (tq > 0 && q == out) return NVFP4_ERR_INVALID_ARG;
   const DeviceInfo dev = current_device();
   if (!dev.ok) return NVFP4_ERR_ARCH;
   if (tq == 0) return NVFP4_OK;

@@ -148,3 +148,26 @@ def test_near_gemm_and_oracle(orc):
     y, yq = nv.gemv(x, q, torch.float32), nv.gemm(qx, q, torch.float32)
     S = xq.double().abs().cpu() @ w.abs().t()
     assert bool(((y - yq).double().abs().cpu() <= far + (2e-3 + 2.0 ** -8) * S).all())
+
+
+@pytest.mark.parametrize("m,xd", [(1, torch.bfloat16), (3, torch.float32), (8, torch.bfloat16),
+                                  (16, torch.float32)])
+@pytest.mark.parametrize("n,k", [(40, 16384), (1000, 8000), (2100, 4128), (5000, 2080)])
+def test_column_splits(m, xd, n, k):
+    """Shapes over which the number of CTAs that split the columns runs from 8 to 1, ragged in
+    rows and columns: against 64 bits, within the bound of x's representation (2^-22 of each
+    256 columns' largest value) and fp32 sums of at most k products in any order."""
+    g = torch.Generator().manual_seed(m * n + k)
+    w = nv.quantize((torch.randn(n, k, generator=g) * 0.1).to(torch.bfloat16).cuda())
+    x = torch.randn(m, k, generator=g).to(xd).cuda()
+    got = nv.gemv(x, w, out_dtype=torch.float32)
+    wd = nv.dequantize(w).double()                     # rounded to bf16
+    err = (got.double() - x.double() @ wd.t()).abs()
+    scale = x.double().abs() @ wd.abs().t()
+    assert bool((err <= scale * 2.0 ** -8).all())      # half a bf16 step of each weight
+    # the splits' sums are one another's up to fp32: rows alone give the same products
+    one = torch.cat([nv.gemv(x[i:i + 1], w, out_dtype=torch.float32) for i in range(m)])
+    top = x.abs().amax(dim=1, keepdim=True).double()
+    tol = scale * 2.0 ** -19 + top * wd.abs().sum(dim=1) * 2.0 ** -21
+    assert bool(((got.double() - one.double()).abs() <= tol).all())
+    assert torch.equal(got, nv.gemv(x, w, out_dtype=torch.float32))

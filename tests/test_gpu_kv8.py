@@ -567,3 +567,48 @@ def test_append_runs_of_all_lengths(heads, dim, page):
     k, v = k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda()
     c.append(k, v, i32(slots))
     _check_append(c, k, v, slots, before)
+
+
+def test_two_streams_at_once():
+    """Two requests' steps at the same time, on a stream each, with clusters, ranges and the
+    workspace of each stream: the same bits as one after the other."""
+    torch.manual_seed(0)
+    caches = [_random_cache(80, 16, 4, 128, s) for s in (1, 2)]
+    w = nv.quantize((torch.randn(512, 1024) * 0.1).to(torch.bfloat16).cuda())
+    table = torch.arange(80).int().cuda().view(1, 80)
+    lens, cu = i32([1270]), i32([0, 1])
+    qs = [torch.randn(1, 8, 128).to(torch.bfloat16).cuda() for _ in range(2)]
+
+    def step(i):
+        c = caches[i]
+        c.append(qs[i][:, :4], qs[i][:, 4:], i32([79 * 16 + 5]))
+        o = c.attention(qs[i], cu, lens, table, max_q=1)
+        return o, nv.gemv(o.view(1, 1024), w)
+    want = [step(i) for i in range(2)]
+    want = [step(i) for i in range(2)]   # (the last page's scale has grown by now)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, y in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(y, want[i][1])
+    for s in streams:
+        with torch.cuda.stream(s):
+            assert nv.device_status() == 0
+
+
+@pytest.mark.parametrize("n", [2, 40])
+def test_output_over_the_queries_is_refused(n):
+    c = _random_cache(8, 16, 2, 64, 3)
+    q = torch.randn(n, 4, 64, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    before = q.clone()
+    with pytest.raises(nv.NVFP4Error):
+        c.attention(q, i32([0, n]), i32([100]), torch.arange(8).int().cuda().view(1, 8), out=q)
+    assert torch.equal(q, before)

@@ -248,3 +248,7 @@ def test_compiled_binding_refuses():
     c.k_codes = c.k_codes[:2]
     with pytest.raises(ValueError):
         c.append(torch.zeros(2, 2, 64).bfloat16(), torch.zeros(2, 2, 64).bfloat16(), i)
+
+
+def test_attention_does_not_write_over_its_queries(L):
+    assert _attention(L, _cache8(), q=FAKE, out=FAKE) == N.ERR_INVALID_ARG
