@@ -202,9 +202,20 @@ PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse(PyExc_ValueError, "plan_pages: more than 2^31 entries");
     const On on(table, "plan_pages");
     const at::Tensor ws = workspace(a[8], table, on);
-    const auto opt = table.options();
-    const at::Tensor seq = at::empty({batch}, opt), cu = at::empty({batch + 1}, opt),
-                     slots = at::empty({max_new}, opt), head_out = at::empty({1}, opt);
+    // the results are parts of one allocation, each on a 16-byte boundary (an allocation costs
+    // as much as half a launch)
+    const int64_t at_cu = (batch + 3) / 4 * 4, at_slots = at_cu + (batch + 4) / 4 * 4,
+                  at_head = at_slots + (int64_t(max_new) + 3) / 4 * 4;
+    const at::Tensor mem = at::empty({at_head + 1}, table.options());
+    auto part = [&mem](int64_t from, int64_t n) {
+      at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(mem.storage()),
+                                                              mem.key_set(), mem.dtype());
+      t.unsafeGetTensorImpl()->set_storage_offset(from);
+      t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+      return t;
+    };
+    const at::Tensor seq = part(0, batch), cu = part(at_cu, batch + 1),
+                     slots = part(at_slots, max_new), head_out = part(at_head, 1);
     auto p = [](const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
     check(lib.plan_pages(p(cached), p(fresh), int32_t(batch), p(table), row_stride(table),
                          int32_t(pages), p(free_pages), int32_t(free_pages.size(0)), p(head),
