@@ -25,11 +25,11 @@
 // A warp takes steps of 32 weight rows by 256 columns (16 rows for the widest x): 128 bytes, a
 // whole line, of each row, copied asynchronously into a ring of its own two steps deep.  (Loads
 // straight into registers, 64 bytes of a row at a time and 16 rows a warp, took 17.4 us for
-// 14336 x 4096 and one row, 13.7 with 32 rows; this takes 11.5, 2.9 TB/s.  Three steps deep
+// 14336 x 4096 and one row, 13.7 with 32 rows; the rings took 11.5 at first.  Three steps deep
 // leaves one CTA an SM: 17 us.)  A CTA has 8 warps: KW of them split the columns (steps dealt out in turn), the
 // other factor 8 / KW takes further rows, which then share the converted x; KW falls with the
-// rows of x, so that the conversion stays a small part of the work.  With KW = 8 a warp
-// converts what it reads itself, and no barrier is needed.  (Converting all of x first, in
+// rows of x, so that the conversion stays a small part of the work.  For one or two rows a warp
+// converts what it reads itself, and no barrier is needed (14336 x 4096: 10.5 us against 11.3).  (Converting all of x first, in
 // a prologue, cost 0.7 us at 1024 x 1024.)  The 16 weight rows of a product are 4 i-values by
 // 4 rows 32 apart: the scale tile of the tensor-core layout keeps their scales in 64
 // contiguous bytes.  Where rows alone leave SMs idle, a cluster of up to 8 CTAs splits the
@@ -37,8 +37,8 @@
 // rank order: no workspace, no atomics, the same result every time.  (Fetching the others' sums
 // instead took 2 us a CTA of the cluster: 7 x 5000 x 14336 in clusters of 6 37 us against 23.)
 //
-// 1 x 1024 x 1024 2.6 us (the launch, one step, the join of the warps); 1 x 14336 x 4096 11.4 us,
-// 44% of the copy rate; 7 x 5000 x 14336 in fp32 22 us, 29%, the conversions' and products'
+// 1 x 1024 x 1024 2.6 us (the launch, one step, the join of the warps); 1 x 14336 x 4096 10.5 us,
+// 48% of the copy rate; 7 x 5000 x 14336 in fp32 22 us, 29%, the conversions' and products'
 // latency with 16 warps an SM.
 #include <algorithm>
 
@@ -137,7 +137,8 @@ template <int KW, int NT>
 constexpr int kJoinBytes = (kWarps / KW * kRowTiles<NT> * 16 * (16 / KW) + kMaxCluster) * 4;
 
 // KW warps split the columns; NT tiles of 8 product columns; FP32 x in two parts.
-template <int KW, int NT, bool FP32>
+// SELF: every warp converts its own x (M <= 2), which needs no barrier.
+template <int KW, int NT, bool FP32, bool SELF>
 __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
   constexpr int kTiles = kRowTiles<NT>;
   constexpr int RG = kWarps / KW;          // groups of 16 kTiles weight rows
@@ -239,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
   Eight xv[kPasses];
   auto pair_of = [&](int p, int& step_of, int& m) {
     const int pair = warp + kWarps * p;
-    step_of = KW == kWarps ? kw : int(fast_div(a.m_div, uint32_t(pair)));
-    m = KW == kWarps ? p : pair - step_of * a.M;
-    return KW == kWarps ? p < a.M : step_of < KW;
+    step_of = SELF ? kw : int(fast_div(a.m_div, uint32_t(pair)));
+    m = SELF ? p : pair - step_of * a.M;
+    return SELF ? p < a.M : step_of < KW;
   };
   auto load_x = [&](int i) {
 #pragma unroll
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
       }
       // columns 64 c + 8 q .. of a step (lane 8 c + q): unit 4 q + c of its row, so that the
       // reads below, lanes c of one q, are 64 contiguous bytes
-      const int pair = step_of * a.M + m;
+      const int pair = (SELF ? warp : step_of) * a.M + m;
       uint8_t* d = xs + (buf * kPairs + pair) * kParts * kXRow + ((lane & 7) * 4 + (lane >> 3)) * 16;
       *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if constexpr (FP32)
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) d[t][n][j] = 0.0f;
     const uint32_t stage = ring + uint32_t(i % kStages) * kStage;
-    const uint8_t* xb = xs + (buf * kPairs + kw * a.M) * kParts * kXRow + c * 16;
+    const uint8_t* xb = xs + (buf * kPairs + (SELF ? warp : kw) * a.M) * kParts * kXRow + c * 16;
     // halves of a lane's 32 bytes: two scale blocks, 8 products each
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int n0 = 8 * n + 2 * c;
-      const float* e = xe[buf] + kw * a.M;
+      const float* e = xe[buf] + (SELF ? warp : kw) * a.M;
       const float e0 = n0 < cols ? e[n0 / kParts] : 0.0f;
       const float e1 = n0 + 1 < cols ? e[(n0 + 1) / kParts] : 0.0f;
 #pragma unroll
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         // the step's weights and x are there; x's buffer j is written again two steps on, after
         // the next barrier, which every reader of this step has then passed
-        if constexpr (KW == kWarps) __syncwarp(); else __syncthreads();
+        if constexpr (SELF) __syncwarp(); else __syncthreads();
         issue(i + kStages - 1);
         if (first + i * stride < n_steps) step(i, j, sc[j]);
         load_s(i + 2, sc[j]);
@@ -508,20 +509,20 @@ int split_of(int ctas, int n_steps, int sm_count, int& cost) {
   return best;
 }
 
-template <int KW, int NT, bool FP32>
+template <int KW, int NT, bool FP32, bool SELF = false>
 cudaError_t launch(const Args& a, int sm_count, cudaStream_t st) {
   const int ctas = ctas_of<KW, NT>(a);
   int cost;
   const int cs = split_of<KW>(ctas, (a.K + kStep - 1) / kStep, sm_count, cost);
   constexpr size_t kSmem = (kRingBytes<NT> + 15) / 16 * 16 + kXBytes<FP32> + kJoinBytes<KW, NT>;
-  const cudaError_t e = allow_smem<gemv_kernel<KW, NT, FP32>>(kSmem);
+  const cudaError_t e = allow_smem<gemv_kernel<KW, NT, FP32, SELF>>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(gemv_kernel<KW, NT, FP32>, dim3(unsigned(ctas * cs)),
+  return launch_pdl_cluster(gemv_kernel<KW, NT, FP32, SELF>, dim3(unsigned(ctas * cs)),
                             dim3(unsigned(cs)), dim3(kThreads), kSmem, st, a);
 }
 
 // One or two rows: all warps on one group of weight rows, or, where that fills the SMs worse,
-// four (1 x 14336 x 4096: 11.5 us with four against 12.2; 1 x 9216 x 5120 9.9 against 7.8).
+// four (1 x 14336 x 4096: 10.6 us with four against 11.8; 1 x 9216 x 5120 13.5 against 7.5).
 bool all_on_one(const Args& a, int sm_count) {
   const int n_steps = (a.K + kStep - 1) / kStep;
   int eight, four;
@@ -551,12 +552,14 @@ cudaError_t launch_gemv(const LaunchGemv& g, cudaStream_t st) {
   // KW M <= 16 row-steps are converted at a time; 8 NT >= product columns
   const bool one = g.M <= 2 && gemv::all_on_one(a, g.sm_count);
   if (g.x_dtype == NVFP4_BF16) {
-    if (one) return gemv::launch<8, 1, false>(a, g.sm_count, st);
+    if (one) return gemv::launch<8, 1, false, true>(a, g.sm_count, st);
+    if (g.M <= 2) return gemv::launch<4, 1, false, true>(a, g.sm_count, st);
     if (g.M <= 4) return gemv::launch<4, 1, false>(a, g.sm_count, st);
     if (g.M <= 8) return gemv::launch<2, 1, false>(a, g.sm_count, st);
     return gemv::launch<1, 2, false>(a, g.sm_count, st);
   }
-  if (one) return gemv::launch<8, 1, true>(a, g.sm_count, st);
+  if (one) return gemv::launch<8, 1, true, true>(a, g.sm_count, st);
+  if (g.M <= 2) return gemv::launch<4, 1, true, true>(a, g.sm_count, st);
   if (g.M <= 4) return gemv::launch<4, 1, true>(a, g.sm_count, st);
   if (g.M <= 8) return gemv::launch<2, 2, true>(a, g.sm_count, st);
   return gemv::launch<1, 4, true>(a, g.sm_count, st);
