@@ -274,6 +274,15 @@ int64_t token_stride(const Cache& c, const at::Tensor& t, int64_t heads, const c
   return t.size(0) > 1 ? t.stride(0) : heads * d;
 }
 
+// (k_codes, v_codes, k_scale, v_scale) -> the codes' shape
+PyObject* kv8_shape(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  NVFP4_CALL({
+    count(n, 4);
+    const Cache c = cache_of(a);
+    return Py_BuildValue("iiii", c.c.n_pages, c.c.kv_heads, c.c.page_tokens, c.c.head_dim);
+  })
+}
+
 // (k_codes, v_codes, k_scale, v_scale, k, v, slot_map, ws)
 PyObject* kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   NVFP4_CALL({
@@ -406,6 +415,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {method<init>("init"),
                          method<gemv>("gemv"),
                          method<plan_pages>("plan_pages"),
+                         method<kv8_shape>("kv8_shape"),
                          method<kv8_append>("kv8_append"),
                          method<kv8_attention>("kv8_attention"),
                          {nullptr, nullptr, 0, nullptr}};

@@ -294,18 +294,9 @@ class KVCache8:
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor):
         """A cache over buffers of the caller's; see empty() for new ones."""
-        shape, dev = k_codes.shape, k_codes.device
-        if len(shape) != 4 or v_codes.shape != shape:
-            raise ValueError("codes must be [n_pages, kv_heads, page_tokens, head_dim]")
-        for t in (k_codes, v_codes):
-            if t.dtype != torch.float8_e4m3fn or not t.is_contiguous() or t.device != dev:
-                raise ValueError("codes must be contiguous float8_e4m3fn tensors on one device")
-        for t in (k_scale, v_scale):
-            if (t.dtype != torch.float32 or t.shape != shape[:2] or not t.is_contiguous() or
-                    t.device != dev):
-                raise ValueError(f"scales must be contiguous fp32 tensors {tuple(shape[:2])}")
+        self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = (
+            _binding or _load_binding()).kv8_shape(k_codes, v_codes, k_scale, v_scale)
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
-        self.n_pages, self.kv_heads, self.page_tokens, self.head_dim = shape
 
     @classmethod
     def empty(cls, n_pages: int, page_tokens: int, kv_heads: int, head_dim: int,
