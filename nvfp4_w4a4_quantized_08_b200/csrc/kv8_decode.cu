@@ -721,7 +721,7 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   p.row_tiles = int32_t((rows + p.rows - 1) / p.rows);
   // Ranges, none shorter than 128 tokens.  Few units: as many as fill one wave of three CTAs
   // an SM (2 x 131072 tokens, 8 heads: 86 us; 93 for four an SM, 107 in 2.7 waves), or the 8
-  // of a cluster where that keeps a range below 512 tokens (1500 tokens, 24 heads: 6.9 us
+  // of a cluster where that keeps a range below 512 tokens (1500 tokens, 24 heads: 6.3 us
   // against 8.3).  Many units: enough ranges for three waves of four CTAs an SM, because
   // lengths differ (64 ragged requests, 8 heads: 90 us in four ranges, 96 in two, 105 in one),
   // until there are two waves of units (200 requests: 76 us whole, 80 in two ranges).
@@ -740,7 +740,7 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   p.n_splits = int32_t((int64_t(d.max_kv) + p.chunk - 1) / p.chunk);
   if (p.n_splits < 1) p.n_splits = 1;
   // In one wave the ranges of a unit can be a cluster, which joins them without a second
-  // kernel (777 tokens, 24 heads: 5.9 us against 7.6); in several, CTAs that wait for their
+  // kernel (777 tokens, 24 heads: 5.4 us against 7.6); in several, CTAs that wait for their
   // cluster hold up others (64 ragged requests: 121 us against 94).
   p.cluster = !p.chunked && p.n_splits > 1 && p.n_splits <= kv8::kMaxCluster && units * p.n_splits <= wave;
   p.scratch = p.n_splits == 1 || p.cluster
