@@ -76,6 +76,7 @@ struct On {
   c10::cuda::OptionalCUDAGuard guard;
   void* stream;
   On(const at::Tensor& t, const char* what) {
+    if (!error_class) refuse(PyExc_RuntimeError, "init has not been called");
     if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(what) + " takes CUDA tensors");
     if (t.get_device() != c10::cuda::current_device()) guard.set_index(t.get_device());
     stream = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
@@ -103,10 +104,10 @@ at::Tensor workspace(PyObject* ws, const at::Tensor& like, const On& on) {
   return it->second;
 }
 
-int32_t dtype_code(const at::Tensor& t) {
-  if (t.scalar_type() == at::kBFloat16) return NVFP4_BF16;
-  if (t.scalar_type() == at::kFloat) return NVFP4_FP32;
-  refuse(PyExc_TypeError, std::string("unsupported dtype ") + toString(t.scalar_type()));
+int32_t dtype_code(at::ScalarType t) {
+  if (t == at::kBFloat16) return NVFP4_BF16;
+  if (t == at::kFloat) return NVFP4_FP32;
+  refuse(PyExc_TypeError, std::string("unsupported dtype ") + toString(t));
 }
 
 // torch gives any stride for a dimension of one
@@ -120,6 +121,12 @@ void int32_tensor(const at::Tensor& t, const at::Device& dev, const char* name, 
     refuse(PyExc_ValueError, std::string(name) + (dims == 1 ? " must be contiguous"
                                                              : " must have unit column stride"));
 }
+
+// Allocations and launches may wait for the GPU, and the GPU for another Python thread.
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
 
 // A refusal or a torch error becomes the Python error.
 #define NVFP4_CALL(...)           \
@@ -148,7 +155,7 @@ PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x.device() != codes.device() || sf.device() != codes.device() ||
         s_t.device() != codes.device())
       refuse(PyExc_ValueError, "x and w must be on one device");
-    const int32_t x_code = dtype_code(x);
+    const int32_t x_code = dtype_code(x.scalar_type());
     at::Tensor out;
     if (a[8] != Py_None) {
       out = tensor(a[8], "out");
@@ -157,21 +164,29 @@ PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
         refuse(PyExc_ValueError, "out must have " + std::to_string(x.size(0)) +
                                      " rows of at least " + std::to_string(rows) +
                                      " unit-stride columns on x's device");
-      dtype_code(out);
+      dtype_code(out.scalar_type());
     }
     const On on(x, "gemv");
-    if (!out.defined()) {
-      if (!THPDtype_Check(a[7])) refuse(PyExc_TypeError, "out_dtype must be a torch.dtype");
-      out = at::empty({x.size(0), rows},
-                      x.options().dtype(reinterpret_cast<THPDtype*>(a[7])->scalar_type));
-    }
+    at::ScalarType type = at::kFloat;
+    if (out.defined())
+      type = out.scalar_type();
+    else if (THPDtype_Check(a[7]))
+      type = reinterpret_cast<THPDtype*>(a[7])->scalar_type;
+    else
+      refuse(PyExc_TypeError, "out_dtype must be a torch.dtype");
+    const int32_t y_code = dtype_code(type), act = int32(a[9], "act");
     const nvfp4_tensor w = {static_cast<uint8_t*>(codes.data_ptr()),
                             static_cast<uint8_t*>(sf.data_ptr()),
                             static_cast<float*>(s_t.data_ptr()), rows, cols,
                             int32(a[6], "sf_layout")};
-    check(lib.gemv(x.data_ptr(), x_code, x.size(0), row_stride(x), &w, out.data_ptr(),
-                   dtype_code(out), row_stride(out), int32(a[9], "act"), on.stream),
-          "nvfp4_gemv");
+    nvfp4_status st;
+    {
+      const NoGil no_gil;
+      if (!out.defined()) out = at::empty({x.size(0), rows}, x.options().dtype(type));
+      st = lib.gemv(x.data_ptr(), x_code, x.size(0), row_stride(x), &w, out.data_ptr(), y_code,
+                    row_stride(out), act, on.stream);
+    }
+    check(st, "nvfp4_gemv");
     return THPVariable_Wrap(out);
   })
 }
@@ -206,7 +221,12 @@ PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     // as much as half a launch)
     const int64_t at_cu = (batch + 3) / 4 * 4, at_slots = at_cu + (batch + 4) / 4 * 4,
                   at_head = at_slots + (int64_t(max_new) + 3) / 4 * 4;
-    const at::Tensor mem = at::empty({at_head + 1}, table.options());
+    const int32_t page_tokens = int32(a[5], "page_tokens"), n_pages = int32(a[6], "n_pages");
+    at::Tensor mem;
+    {
+      const NoGil no_gil;
+      mem = at::empty({at_head + 1}, table.options());
+    }
     auto part = [&mem](int64_t from, int64_t n) {
       at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(mem.storage()),
                                                               mem.key_set(), mem.dtype());
@@ -217,12 +237,15 @@ PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor seq = part(0, batch), cu = part(at_cu, batch + 1),
                      slots = part(at_slots, max_new), head_out = part(at_head, 1);
     auto p = [](const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
-    check(lib.plan_pages(p(cached), p(fresh), int32_t(batch), p(table), row_stride(table),
-                         int32_t(pages), p(free_pages), int32_t(free_pages.size(0)), p(head),
-                         int32(a[5], "page_tokens"), int32(a[6], "n_pages"), p(seq), p(cu),
-                         p(slots), max_new, p(head_out), ws.data_ptr(), size_t(ws.numel()),
-                         on.stream),
-          "nvfp4_plan_pages");
+    nvfp4_status st;
+    {
+      const NoGil no_gil;
+      st = lib.plan_pages(p(cached), p(fresh), int32_t(batch), p(table), row_stride(table),
+                          int32_t(pages), p(free_pages), int32_t(free_pages.size(0)), p(head),
+                          page_tokens, n_pages, p(seq), p(cu), p(slots), max_new, p(head_out),
+                          ws.data_ptr(), size_t(ws.numel()), on.stream);
+    }
+    check(st, "nvfp4_plan_pages");
     PyObject* r = PyTuple_New(4);
     if (!r) return nullptr;
     PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(seq));
@@ -300,10 +323,14 @@ PyObject* kv8_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
              "slot_map must have at least " + std::to_string(tokens) + " entries");
     const On on(k, "append");
     const at::Tensor ws = workspace(a[7], k, on);
-    check(lib.append(&c.c, k.data_ptr(), v.data_ptr(), stride, tokens,
-                     static_cast<const int32_t*>(slots.data_ptr()), ws.data_ptr(),
-                     size_t(ws.numel()), on.stream),
-          "nvfp4_kv8_append");
+    nvfp4_status st;
+    {
+      const NoGil no_gil;
+      st = lib.append(&c.c, k.data_ptr(), v.data_ptr(), stride, tokens,
+                      static_cast<const int32_t*>(slots.data_ptr()), ws.data_ptr(),
+                      size_t(ws.numel()), on.stream);
+    }
+    check(st, "nvfp4_kv8_append");
     Py_RETURN_NONE;
   })
 }
@@ -358,20 +385,24 @@ PyObject* kv8_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (PyErr_Occurred()) throw Refused();
     }
     const On on(q, "attention");
-    if (!out.defined()) out = at::empty({tokens, heads, d}, q.options());
     const int want_lse = PyObject_IsTrue(a[13]);
     if (want_lse < 0) throw Refused();
-    if (want_lse) lse = at::empty({tokens, heads}, q.options().dtype(at::kFloat));
     const at::Tensor ws = workspace(a[14], q, on);
-    const size_t need = lib.scratch_bytes(&c.c, &b, tokens, int32_t(heads), causal);
-    // a tensor of the call's own: calls on other streams and captured graphs share nothing
-    if (need) scratch = at::empty({int64_t(need)}, q.options().dtype(at::kByte));
-    check(lib.attention(&c.c, &b, q.data_ptr(), stride, tokens, int32_t(heads), causal, scale,
-                        out.data_ptr(), out_stride,
-                        want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                        need ? scratch.data_ptr() : nullptr, need, ws.data_ptr(),
-                        size_t(ws.numel()), on.stream),
-          "nvfp4_kv8_attention");
+    nvfp4_status st;
+    {
+      const NoGil no_gil;
+      if (!out.defined()) out = at::empty({tokens, heads, d}, q.options());
+      if (want_lse) lse = at::empty({tokens, heads}, q.options().dtype(at::kFloat));
+      const size_t need = lib.scratch_bytes(&c.c, &b, tokens, int32_t(heads), causal);
+      // a tensor of the call's own: calls on other streams and captured graphs share nothing
+      if (need) scratch = at::empty({int64_t(need)}, q.options().dtype(at::kByte));
+      st = lib.attention(&c.c, &b, q.data_ptr(), stride, tokens, int32_t(heads), causal, scale,
+                         out.data_ptr(), out_stride,
+                         want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+                         need ? scratch.data_ptr() : nullptr, need, ws.data_ptr(),
+                         size_t(ws.numel()), on.stream);
+    }
+    check(st, "nvfp4_kv8_attention");
     if (!want_lse) return THPVariable_Wrap(out);
     PyObject* r = PyTuple_New(2);
     if (!r) return nullptr;

@@ -612,3 +612,33 @@ def test_output_over_the_queries_is_refused(n):
     with pytest.raises(nv.NVFP4Error):
         c.attention(q, i32([0, n]), i32([100]), torch.arange(8).int().cuda().view(1, 8), out=q)
     assert torch.equal(q, before)
+
+
+def test_two_threads():
+    """Python threads with a stream each call at the same time: the same bits as alone."""
+    import threading
+    caches = [_random_cache(64, 16, 2, 64, s) for s in (5, 6)]
+    table = torch.arange(64).int().cuda().view(2, 32)
+    lens, cu, free, head = i32([400, 37]), i32([0, 1, 2]), i32([63]), i32([0])
+    qs = [torch.randn(2, 8, 64, generator=torch.Generator().manual_seed(s)).to(torch.bfloat16)
+          .cuda() for s in range(2)]
+    want = [c.attention(q, cu, lens, table, return_lse=True) for c, q in zip(caches, qs)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(200):
+                p = nv.plan_pages(lens, i32([0, 0]), table, free, head, 16, 64, 0)
+                o, l = caches[i].attention(qs[i], cu, p.seq_lens, table, return_lse=True)
+                if not (torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])):
+                    wrong.append(i)
+            if nv.device_status() != 0:
+                wrong.append("status")
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
