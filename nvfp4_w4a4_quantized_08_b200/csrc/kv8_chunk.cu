@@ -350,10 +350,14 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           float factor = 1.0f;
           if (mx - kBias > ref + kLazy || !seen) {
             if (mx > -INFINITY) {
-              factor = seen ? exp2_approx(ref - (mx - kBias)) : 0.0f;
+              // In two steps: the reference may rise by more than 2^126 through the pages' V scales
+              // alone, after tokens that still are most of the normaliser (O in units of the largest
+              // weight is lost then, the normaliser is not).
+              const float half = seen ? exp2_approx(0.5f * (ref - (mx - kBias))) : 0.0f;
+              factor = half * half;
               ref = mx - kBias;
               seen = true;
-              l_run *= factor;
+              l_run = l_run * half * half;
             }
           }
           all_seen = __all_sync(0xFFFFFFFFu, seen);

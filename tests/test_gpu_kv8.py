@@ -1,5 +1,6 @@
 """GPU parity of the paged 8-bit cache: page plans (exact), the quantizing write (exact codes and
 scales) and the attention (tests/_kv8.py's bounds), alone and together."""
+import math
 import random
 
 import pytest
@@ -642,3 +643,29 @@ def test_two_threads():
     for t in threads:
         t.join()
     assert not wrong
+
+
+# ---------------------------------------------------------------- the ends of the ranges
+@pytest.mark.parametrize("max_kv", [1, None])   # one range, or several that are joined
+@pytest.mark.parametrize("nq", [1, 33, 200])
+@pytest.mark.parametrize("before,e,rise", [(1536, 60, 7), (10240, 55, 17), (1536, 60, 100),
+                                           (256, 60, -7), (128, 0, 130)])
+def test_v_scales_at_both_ends_of_the_range(before, e, rise, nq, max_kv):
+    """V scales 2^-e, then 2^e for one last token whose score is larger (base 2): the normaliser of
+    the tokens before has to survive, however far the weights' reference rises."""
+    n = before // 16
+    c = _random_cache(n + 1, 16, 1, 64, 25, spread=0)
+    codes = c.k_codes.view(torch.uint8)
+    codes[:] = 0
+    codes[n, 0, 0, 0] = 0x38 if rise > 0 else 0xB8             # +-1.0
+    c.k_scale[:] = 1.0
+    c.v_scale[:n], c.v_scale[n] = 2.0 ** -e, 2.0 ** e
+    q = torch.zeros(nq, 1, 64, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    scale = abs(rise) * math.log(2)
+    table = list(range(n + 1))
+    o, lse = c.attention(q, i32([0, nq]), i32([before + 1]), i32([table]), causal=False, max_q=nq,
+                         max_kv=max_kv, scale=scale, return_lse=True)
+    want = ref.attention(q.cpu().double(), *_planes64(c), [table], [nq], [before + 1], 16, False,
+                         scale)
+    ref.assert_attention_close(o, lse, want)
