@@ -321,10 +321,13 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           if (!again) l_run += l;
         }
         if (again) {
-          // The slower form, until every row has seen a token, for masked tiles (exact zeros), V scales far from 1,
-          // and a new maximum: the reference rises to it, l and O are rescaled, and the V scale
-          // is multiplied in after the exponential, so that a token counts for the normaliser
-          // even where its weight is lost against the largest.
+          // The slower form, until every row has seen a token, for masked tiles (exact zeros), V
+          // scales far from 1, and a new maximum: the reference rises to it, l and O are
+          // rescaled, and the V scale is multiplied in after the exponential, so that a token
+          // counts for the normaliser even where its weight is lost against the largest.  A masked
+          // score is -inf, so no factor may be 0: K scales are where a page was never written, and
+          // small ones times the power of two of a row near 0 underflow.
+          auto factor_of = [&](int n) { return fmaxf(ms[n] * q_scale, 0x1p-126f); };
           if (vis_min < (j + 1) * kKeys) {
             const int left = vis - j * kKeys;
 #pragma unroll
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 t1 = max3f(t1, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
             }
             // (the scales are positive; a group of no page has a log2 of -inf)
-            mx = fmaxf(mx, fmaf(fmaxf(t0, t1), ms[n] * q_scale, ms[kGroups + n]));
+            mx = fmaxf(mx, fmaf(fmaxf(t0, t1), factor_of(n), ms[kGroups + n]));
           }
           float factor = 1.0f;
           if (mx - kBias > ref + kLazy || !seen) {
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
             uint32_t pk[16];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              const float scn = ms[2 * c + n] * q_scale;
+              const float scn = factor_of(2 * c + n);
               // a group of no page: 0 for the normaliser too
               const float lv = ms[kGroups + 2 * c + n];
               const float none = lv == -INFINITY ? -INFINITY : -ref, sv = exp2f(lv);
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const float lv = float(int(bits >> 23) - 127) +
                          __log2f(__uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
         if (t < kGroups) {
-          m[0] = none ? 1.0f : ks * a.scale_log2;   // (not 0: a masked score is -inf)
+          m[0] = none ? 1.0f : ks * a.scale_log2;
           m[kGroups] = none ? -INFINITY : lv;
           m[2 * kGroups] = none ? 0.0f : 1.0f / v;
         }

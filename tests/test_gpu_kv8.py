@@ -669,3 +669,39 @@ def test_v_scales_at_both_ends_of_the_range(before, e, rise, nq, max_kv):
     want = ref.attention(q.cpu().double(), *_planes64(c), [table], [nq], [before + 1], 16, False,
                          scale)
     ref.assert_attention_close(o, lse, want)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq", [1, 12, 40])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_pages_never_written(dim, nq, causal):
+    """A new cache (scales of 0), as a warm-up before the first tokens meets it: zeros, and the
+    log-sum-exp of equal scores."""
+    c = nv.KVCache8.empty(8, 16, 2, dim)
+    q = torch.randn(2 * nq, 6, dim, generator=torch.Generator().manual_seed(1))
+    q = q.to(torch.bfloat16).cuda()
+    table, kv = [[0, 1, 2, 3], [4, 5, 6, 7]], [50, 17]
+    o, lse = c.attention(q, i32([0, nq, 2 * nq]), i32(kv), i32(table), causal=causal, max_q=nq,
+                         return_lse=True)
+    want = ref.attention(q.cpu().double(), *_planes64(c), table, [nq, nq], kv, 16, causal,
+                         dim ** -0.5)
+    ref.assert_attention_close(o, lse, want)
+    assert not o.any()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("nq", [1, 8, 9, 40, 300])
+@pytest.mark.parametrize("mult", [0.0, 2.0 ** -130, 1.0])
+def test_zero_keys_and_zero_or_tiny_queries(nq, mult, causal):
+    """K of zeros gets the smallest scale there is; with q near 0 too, score factors underflow:
+    every token weighs the same."""
+    c = nv.KVCache8.empty(8, 16, 1, 64)
+    g = torch.Generator().manual_seed(2)
+    v = torch.randn(67, 1, 64, generator=g).to(torch.bfloat16).cuda()
+    c.append(torch.zeros_like(v), v, i32(list(range(50)) + list(range(80, 97))))
+    q = (torch.randn(2 * nq, 4, 64, generator=g) * mult).to(torch.bfloat16).cuda()
+    table, kv = [[0, 1, 2, 3], [5, 6, 7]], [50, 17]
+    o, lse = c.attention(q, i32([0, nq, 2 * nq]), i32(kv), i32([table[0], table[1] + [0]]),
+                         causal=causal, max_q=nq, return_lse=True)
+    want = ref.attention(q.cpu().double(), *_planes64(c), table, [nq, nq], kv, 16, causal, 0.125)
+    ref.assert_attention_close(o, lse, want)
