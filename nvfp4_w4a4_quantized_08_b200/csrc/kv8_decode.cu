@@ -511,7 +511,8 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>) decode_kernel(const A
       mt = fmaxf(mt, sm[w][0][row]);
       mvt = fmaxf(mvt, sm[w][1][row]);
     }
-    const float top = mt == kNegInf ? 0.0f : mt, topv = mvt == kNegInf ? 0.0f : mvt;
+    // (no weights: all V scales are 0; then 2^(topv - top) is kept from overflowing)
+    const float top = mt == kNegInf ? 0.0f : mt, topv = mvt == kNegInf ? top : mvt;
     float sum = 0.0f, f[kWarps];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {

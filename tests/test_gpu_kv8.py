@@ -705,3 +705,21 @@ def test_zero_keys_and_zero_or_tiny_queries(nq, mult, causal):
                          causal=causal, max_q=nq, return_lse=True)
     want = ref.attention(q.cpu().double(), *_planes64(c), table, [nq, nq], kv, 16, causal, 0.125)
     ref.assert_attention_close(o, lse, want)
+
+
+@pytest.mark.parametrize("kv", [40, 3000])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_v_scales_of_zero_under_low_scores(nq, kv):
+    """V pages never written beside K pages that were, all scores far below 0: zeros, no NaN."""
+    n = -(-kv // 16)
+    c = _random_cache(n, 16, 1, 64, 26, spread=0)
+    c.v_scale.zero_()
+    c.v_codes.view(torch.uint8)[:] = 0
+    c.k_codes.view(torch.uint8)[:] = 0x38
+    c.k_scale[:] = 1.0
+    q = torch.full((nq, 4, 64), -40.0, dtype=torch.bfloat16, device="cuda")
+    table = list(range(n))
+    o, lse = c.attention(q, i32([0, nq]), i32([kv]), i32([table]), causal=False, max_q=nq,
+                         return_lse=True)
+    want = ref.attention(q.cpu().double(), *_planes64(c), [table], [nq], [kv], 16, False, 0.125)
+    ref.assert_attention_close(o, lse, want)
