@@ -299,6 +299,8 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
         if constexpr (FP32) {
           const __half2 h = *reinterpret_cast<const __half2*>(&hi[i]);
           lo[i] = f16x2_rn((u - __low2float(h)) * 2048.0f, (v - __high2float(h)) * 2048.0f);
+          // an infinity is whole in its first part (inf - inf is not)
+          if (top >= 0x7F800000u) lo[i] = 0;
         }
       }
       // columns 64 c + 8 q .. of a step (lane 8 c + q): unit 4 q + c of its row, so that the

@@ -171,3 +171,29 @@ def test_column_splits(m, xd, n, k):
     tol = scale * 2.0 ** -19 + top * wd.abs().sum(dim=1) * 2.0 ** -21
     assert bool(((got.double() - one.double()).abs() <= tol).all())
     assert torch.equal(got, nv.gemv(x, w, out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("xd", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m", [1, 2, 3, 7, 16])
+def test_infinities_and_nan(orc, m, xd):
+    """An infinite x gives infinities (NaN against a weight of zero, or another infinity's
+    opposite), a NaN gives NaN, in its row alone."""
+    n, k = 70, 544
+    q, w = _weights(orc, n, k, nv.SF_MMA128x4, 13)
+    inf = float("inf")
+    x = torch.randn(m, k, generator=torch.Generator().manual_seed(m))
+    x[0, 5] = inf
+    if m > 2:
+        x[2, 300], x[2, 301] = -inf, inf
+    if m > 3:
+        x[3, 40], x[4, 543], x[5, 7] = float("nan"), -inf, inf
+        x[5, :256].fill_(inf)
+    x = x.to(xd).cuda()
+    for dt in (torch.float32, torch.bfloat16):
+        got = nv.gemv(x, q, dt).double().cpu()
+        want = (x.double().cpu()[:, None] * w[None]).sum(2)
+        assert torch.equal(got.isnan(), want.isnan())
+        assert torch.equal(got == inf, want == inf) and torch.equal(got == -inf, want == -inf)
+        good = x.isfinite().all(1)
+        if bool(good.any()):
+            _check(got[good.cpu()], x[good], w, dt == torch.bfloat16)
