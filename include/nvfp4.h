@@ -335,8 +335,9 @@ NVFP4_API int64_t nvfp4_sink_plan_frame_of_slot(const nvfp4_sink_plan* plan, int
  *        2^-33 of it below; fp32 values within 2^-22 relative, or 2^-43 of it below.
  *   W:   N x K weights, either scale layout; K a multiple of 32.
  *   y:   device, bf16 or fp32 (y_dtype), row stride ldy >= N elements; memory of its own.
- *   act: nvfp4_act.  The GELU takes y rounded to bf16 for bf16 output, and uses the
- *        exact tanh to fp32 accuracy (not the approximation of nvfp4_gemm).
+ *   act: nvfp4_act.  The GELU takes y rounded to bf16 for bf16 output, and is right to
+ *        2^-24 (8 + 14 |u|) of itself, u = sqrt(2/pi) (y + 0.044715 y^3), or 0 below 2^-124
+ *        (in fp32; not the approximation of nvfp4_gemm).
  * No workspace; the result does not depend on timing.
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, ARCH, CUDA. */
 #define NVFP4_GEMV_MAX_ROWS 16

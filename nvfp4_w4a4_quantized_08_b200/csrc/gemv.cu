@@ -116,8 +116,10 @@ __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
 }
 
 __device__ __forceinline__ float gelu_tanh(float y) {
+  // y (1 + tanh u) / 2 = y / (1 + exp(-2u)), without the cancellation for y below 0 (there 1 + tanh u
+  // has no more than the last bits of 1); exp overflows to inf where the result is -0
   const float u = 0.7978845608028654f * (y + 0.044715f * y * y * y);
-  return 0.5f * y * (1.0f + tanhf(u));
+  return y / (1.0f + expf(-2.0f * u));
 }
 
 // Products of 16 weight rows per warp (one where four tiles of columns fill the registers).

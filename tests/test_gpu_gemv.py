@@ -197,3 +197,29 @@ def test_infinities_and_nan(orc, m, xd):
         good = x.isfinite().all(1)
         if bool(good.any()):
             _check(got[good.cpu()], x[good], w, dt == torch.bfloat16)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_gelu_of_negative_values(bf16):
+    """The GELU from -8 to 0, where it falls to 1e-14: right relative to itself.  y is exact here
+    (one product of short significands); u = sqrt(2 / pi) (y + 0.044715 y^3) takes seven roundings,
+    constants included, which reach the result through exp(-2u) as 14 |u| 2^-24; the exponential,
+    the sum and the quotient add at most 8 2^-24."""
+    code = torch.zeros(7, 16, dtype=torch.uint8)
+    code[:, 0] = torch.arange(1, 8)                       # 0.5 .. 6 in the first column
+    q = nv.NVFP4Tensor(code.cuda(), torch.full((14,), 0x38, dtype=torch.uint8, device="cuda"),
+                       torch.ones(1, device="cuda"), 7, 32, nv.SF_ROWMAJOR)
+    x = torch.zeros(16, 32)
+    x[:, 0] = -torch.arange(1, 17) / 12.0
+    x = x.to(torch.bfloat16).float()
+    y = (x[:, :1] * E2M1[1:8].float()).double()
+    if bf16:
+        y = y.to(torch.bfloat16).double()
+    u = (2 / torch.pi) ** 0.5 * (y + 0.044715 * y ** 3)
+    want = y / (1 + torch.exp(-2 * u))
+    tol = 2.0 ** -24 * (8 + 14 * u.abs()) * want.abs()
+    if bf16:
+        tol = tol + 2.0 ** -8 * (want.abs() + tol)
+    got = nv.gemv(x.cuda(), q, torch.bfloat16 if bf16 else torch.float32, act=nv.ACT_GELU_TANH)
+    err = (got.double().cpu() - want).abs()
+    assert bool((err <= tol).all()), float((err / tol).max())
