@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
   __shared__ unsigned long long totals[2];
   __shared__ int32_t bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int step = gridDim.x * kThreads, g = blockIdx.x * kThreads + tid;
   if (tid == 0) bad = 0, totals[0] = 0, totals[1] = 0;
   pdl_wait();
   pdl_trigger();
@@ -106,10 +107,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
       record_status(a.status, (fault & 1) ? NVFP4_ERR_INVALID_ARG : NVFP4_ERR_CAPACITY);
       *a.free_head_out = head;
     }
-    const int step = gridDim.x * kThreads, g = blockIdx.x * kThreads + tid;
     for (int i = g; i < a.batch; i += step) a.seq_lens[i] = a.cached[i];
     for (int i = g; i <= a.batch; i += step) a.cu_new[i] = 0;
-    for (int i = g; i < a.max_new; i += step) a.slot_map[i] = -1;
+    for (uint32_t i = g; i < uint32_t(a.max_new); i += step) a.slot_map[i] = -1;
     return;
   }
   for (int b = b0; b < b1; ++b) {
@@ -122,7 +122,6 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
   __syncthreads();
 
   // lengths and offsets
-  const int step = gridDim.x * kThreads, g = blockIdx.x * kThreads + tid;
   for (int i = g; i <= a.batch; i += step) {
     a.cu_new[i] = cu[i];
     if (i < a.batch) a.seq_lens[i] = a.cached[i] + a.fresh[i];
@@ -135,8 +134,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
     for (int i = held + lane; i < total; i += 32)
       a.table[b * a.table_stride + i] = a.free_pages[first[b] + i - held];
   }
-  // slots: the request by bisection of cu, its page from the free list or the table
-  for (int t = g; t < a.max_new; t += step) {
+  // slots: the request by bisection of cu, its page from the free list or the table (unsigned: the
+  // last t + step may be past 2^31)
+  for (uint32_t i = g; i < uint32_t(a.max_new); i += step) {
+    const int t = int(i);
     int32_t slot = -1;
     if (t < int(all_tokens)) {
       int lo = 0, hi = a.batch;  // the last b with cu[b] <= t
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
       else
         record_status(a.status, NVFP4_ERR_INVALID_ARG);
     }
-    a.slot_map[t] = slot;
+    a.slot_map[i] = slot;
   }
 }
 

@@ -723,3 +723,18 @@ def test_v_scales_of_zero_under_low_scores(nq, kv):
                          return_lse=True)
     want = ref.attention(q.cpu().double(), *_planes64(c), [table], [nq], [kv], 16, False, 0.125)
     ref.assert_attention_close(o, lse, want)
+
+
+@pytest.mark.parametrize("fits", [True, False])
+def test_plan_with_the_largest_slot_map(fits):
+    """2^31 - 1 slots: the loops over them step past 2^31."""
+    p = nv.plan_pages(i32([20, 0]), i32([3, 20 if fits else -1]), i32([[0, 1], [-1, -1]]),
+                      i32([5, 4]), i32([0]), page_tokens=16, n_pages=6, max_new=2 ** 31 - 1)
+    want = [20, 21, 22, *range(80, 96), *range(64, 68)] if fits else [-1] * 23
+    assert p.slot_map[:23].tolist() == want and p.slot_map.numel() == 2 ** 31 - 1
+    assert p.cu_new.tolist() == ([0, 3, 23] if fits else [0, 0, 0])
+    assert p.seq_lens.tolist() == ([23, 20] if fits else [20, 0])
+    assert p.free_head.tolist() == [2 if fits else 0]
+    for at in range(23, 2 ** 31 - 1, 1 << 28):
+        assert bool((p.slot_map[at:at + (1 << 28)] == -1).all())
+    assert nv.device_status() == (N.OK if fits else N.ERR_INVALID_ARG)
