@@ -399,6 +399,7 @@ typedef struct {
 #define NVFP4_KV8_MIN_EXP (-60)
 #define NVFP4_KV8_MAX_EXP 60
 #define NVFP4_KV8_MAX_SPLITS 128
+#define NVFP4_KV8_MAX_TOKENS 0x7FFF0000
 
 /* Write new tokens into the cache.  The new tokens of one page and head get the scale
  *   s = 2^e, e the smallest in [-60, 60] with max|x| <= 448 * 2^e,
@@ -424,7 +425,9 @@ NVFP4_API nvfp4_status nvfp4_kv8_append(const nvfp4_kv8_cache* cache, const void
 /* The queries and the cached tokens of a batch of requests.
  *   cu_q:        device [batch + 1], request b has the queries cu_q[b] .. cu_q[b+1] - 1
  *   kv_lens:     device [batch], tokens in the cache (its new ones included)
- *   block_table: device [batch][table_stride], max_pages entries used a row
+ *   block_table: device [batch][table_stride], max_pages entries used a row, max_pages *
+ *                page_tokens at most NVFP4_KV8_MAX_TOKENS (the kernels look some thousand
+ *                tokens ahead in 32 bits)
  *   max_q:       host, no request has more queries
  *   max_kv:      host, about the largest kv_lens: how the work is split goes by it, the
  *                result holds for any value >= 1 */

@@ -99,7 +99,7 @@ nvfp4_status check_kv8_batch(const nvfp4_kv8_cache* c, const nvfp4_kv8_batch* b,
   if (q_heads % c->kv_heads != 0) return NVFP4_ERR_INVALID_ARG;
   if (b->batch > 65535 || tq * q_heads >= (int64_t(1) << 31) ||
       int64_t(b->max_q) * q_heads >= (int64_t(1) << 31) ||
-      int64_t(b->max_pages) * c->page_tokens >= (int64_t(1) << 31))
+      int64_t(b->max_pages) * c->page_tokens > NVFP4_KV8_MAX_TOKENS)
     return NVFP4_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(b->cu_q, 4) || !aligned(b->kv_lens, 4) || !aligned(b->block_table, 4))
     return NVFP4_ERR_MISALIGNED;

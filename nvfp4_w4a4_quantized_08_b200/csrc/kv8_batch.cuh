@@ -59,7 +59,7 @@ __device__ __forceinline__ int sees(const Args& a, const Request& r, int rho) {
 
 // Ranges of a request of kv tokens (at least one; the last takes what is left).
 __device__ __forceinline__ int splits_of(const Args& a, int kv) {
-  return max(1, min(a.n_splits, (kv + a.chunk - 1) / a.chunk));
+  return max(1, min(a.n_splits, int((uint32_t(kv) + a.chunk - 1) / uint32_t(a.chunk))));
 }
 
 __device__ __forceinline__ const uint16_t* q_row(const Args& a, const Request& r, int h, int rho,

@@ -252,3 +252,14 @@ def test_compiled_binding_refuses():
 
 def test_attention_does_not_write_over_its_queries(L):
     assert _attention(L, _cache8(), q=FAKE, out=FAKE) == N.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("page", [16, 64, 4096])
+def test_attention_rejects_tables_too_wide_for_its_look_ahead(L, page):
+    """The kernels read table entries of up to 64 steps of 64 tokens past a range: their 32-bit token
+    numbers must not wrap there (a negative one would pass for a small one)."""
+    most = 0x7FFF0000 // page
+    assert most * page + 4096 + 128 < 2 ** 31 <= (2 ** 31 // page - 1) * page + 4096 + 128
+    for pages in (most + 1, 2 ** 31 // page - 1):
+        assert _attention(L, _cache8(page=page), pages=pages, stride=pages, max_kv=2 ** 31 - 1) == \
+            N.ERR_UNSUPPORTED_SHAPE
