@@ -334,7 +334,8 @@ NVFP4_API int64_t nvfp4_sink_plan_frame_of_slot(const nvfp4_sink_plan* plan, int
  *        largest magnitude there: bf16 values exactly down to 2^-22 of it and within
  *        2^-33 of it below; fp32 values within 2^-22 relative, or 2^-43 of it below.
  *   W:   N x K weights, either scale layout; K a multiple of 32.
- *   y:   device, bf16 or fp32 (y_dtype), row stride ldy >= N elements; memory of its own.
+ *   y:   device, bf16 or fp32 (y_dtype), row stride ldy >= N elements; memory of its own
+ *        (rows beside those of x in one buffer, at one stride, are; overlaps are refused).
  *   act: nvfp4_act.  The GELU takes y rounded to bf16 for bf16 output, and is right to
  *        2^-24 (8 + 14 |u|) of itself, u = sqrt(2/pi) (y + 0.044715 y^3), or 0 below 2^-124
  *        (in fp32; not the approximation of nvfp4_gemm).
@@ -451,9 +452,12 @@ typedef struct {
  *   q:   device bf16, tq tokens at q_token_stride elements (>= q_heads * head_dim, a
  *        multiple of 8), q_heads x head_dim contiguous in a token; 16-byte aligned.
  *   q_heads: a multiple of kv_heads.
- *   out: device bf16, same layout at out_token_stride, memory of its own (not q's: a row of
- *        q is read by several blocks).  Rows of no request are left.
- *   lse: NULL, or device floats [tq][q_heads]: the natural log-sum-exp of a row's scores.
+ *   out: device bf16, same layout at out_token_stride, memory of its own (a row of q is read
+ *        by several blocks; tokens beside those of q in one buffer, at one stride, are apart
+ *        from them).  Rows of no request are left.
+ *   lse: NULL, or device floats [tq][q_heads]: the natural log-sum-exp of a row's scores;
+ *        memory of its own.  Overlaps of out, lse and scratch with what is read, or with one
+ *        another, are refused.
  *   scratch: device, nvfp4_kv8_attention_scratch_bytes(...) bytes, 16-byte aligned (NULL
  *        where that is 0); free for other use once the call's work is done.
  *   ws:  device workspace (status word).

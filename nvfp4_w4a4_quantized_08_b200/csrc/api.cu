@@ -40,6 +40,31 @@ DeviceInfo current_device() {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// n rows of `width` bytes, `stride` bytes apart (at least width).
+struct Rows {
+  const void* p;
+  int64_t n, width, stride;
+};
+Rows block(const void* p, int64_t bytes) { return {p, 1, bytes, bytes}; }
+
+// Whether two sets of rows share a byte.  Rows of one stride may lie beside each other (parts of a
+// fused projection); where the strides differ, sets whose spans meet count as sharing.
+bool overlap(Rows a, Rows b) {
+  if (!a.p || !b.p || a.n <= 0 || b.n <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const int64_t a0 = int64_t(reinterpret_cast<uintptr_t>(a.p));
+  const int64_t b0 = int64_t(reinterpret_cast<uintptr_t>(b.p));
+  if (a0 + (a.n - 1) * a.stride + a.width <= b0 || b0 + (b.n - 1) * b.stride + b.width <= a0)
+    return false;
+  if (a.n == 1) a.stride = b.stride;
+  if (b.n == 1) b.stride = a.stride;
+  const int64_t s = a.stride;
+  if (b.stride != s || a.width > s || b.width > s) return true;
+  // row j of b begins in row j + r of a, `at` bytes behind its start, and may run into the next
+  const int64_t d = b0 - a0, at = (d % s + s) % s, r = (d - at) / s;
+  auto meet = [&](int64_t shift) { return shift < a.n && shift + b.n > 0; };
+  return (at < a.width && meet(r)) || (at + b.width > s && meet(r + 1));
+}
+
 nvfp4_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
 bool valid_layout(int32_t l) { return l == NVFP4_SF_ROWMAJOR || l == NVFP4_SF_MMA128x4; }
@@ -414,6 +439,13 @@ nvfp4_status nvfp4_gemv(const void* x, int32_t x_dtype, int64_t m, int64_t ldx,
   const int64_t xsz = x_dtype == NVFP4_BF16 ? 2 : 4, ysz = y_dtype == NVFP4_BF16 ? 2 : 4;
   if (!aligned(x, 16) || (ldx * xsz) % 16 != 0 || !aligned(y, uintptr_t(ysz)))
     return NVFP4_ERR_MISALIGNED;
+  // y is written while other blocks still read x and W
+  const Rows out = {y, m, W->rows * ysz, ldy * ysz};
+  if (overlap(out, {x, m, W->cols * xsz, ldx * xsz}) ||
+      overlap(out, block(W->codes, int64_t(nvfp4_codes_bytes(W->rows, W->cols)))) ||
+      overlap(out, block(W->sf, int64_t(nvfp4_sf_bytes(W->rows, W->cols, W->sf_layout)))) ||
+      overlap(out, block(W->s_t, 4)))
+    return NVFP4_ERR_INVALID_ARG;
   const DeviceInfo dev = current_device();
   if (!dev.ok) return NVFP4_ERR_ARCH;
   LaunchGemv g;
@@ -559,13 +591,30 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
     return NVFP4_ERR_MISALIGNED;
   if (!ws || ws_bytes < kWsBytes) return NVFP4_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return NVFP4_ERR_MISALIGNED;
-  if (tq > 0 && q == out) return NVFP4_ERR_INVALID_ARG;
+  // what is written has to be apart from what other blocks still read
+  const Rows rows_out = {out, tq, row * 2, out_token_stride * 2};
+  const Rows rows_lse = block(lse, tq * q_heads * 4);
+  const int64_t scales = int64_t(cache->n_pages) * cache->kv_heads;
+  const int64_t codes = scales * cache->page_tokens * cache->head_dim;
+  const Rows read[] = {
+      {q, tq, row * 2, q_token_stride * 2}, block(cache->k_codes, codes),
+      block(cache->v_codes, codes), block(cache->k_scale, scales * 4),
+      block(cache->v_scale, scales * 4), block(batch->cu_q, (int64_t(batch->batch) + 1) * 4),
+      block(batch->kv_lens, int64_t(batch->batch) * 4),
+      {batch->block_table, batch->batch, int64_t(batch->max_pages) * 4, batch->table_stride * 4}};
+  for (const Rows& r : read)
+    if (overlap(rows_out, r) || overlap(rows_lse, r)) return NVFP4_ERR_INVALID_ARG;
+  if (overlap(rows_out, rows_lse)) return NVFP4_ERR_INVALID_ARG;
   const DeviceInfo dev = current_device();
   if (!dev.ok) return NVFP4_ERR_ARCH;
   if (tq == 0) return NVFP4_OK;
   LaunchKv8Attn d = kv8_args(cache, batch, tq, q_heads, causal, dev.sm_count);
   const size_t need = kv8_plan(d).scratch;
   if (need > 0 && (!scratch || scratch_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  if (overlap(block(scratch, int64_t(need)), rows_out) ||
+      overlap(block(scratch, int64_t(need)), rows_lse) ||
+      overlap(block(scratch, int64_t(need)), read[0]))
+    return NVFP4_ERR_INVALID_ARG;
   d.q = q;
   d.q_stride = q_token_stride;
   d.out = out;

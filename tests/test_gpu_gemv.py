@@ -223,3 +223,20 @@ def test_gelu_of_negative_values(bf16):
     got = nv.gemv(x.cuda(), q, torch.bfloat16 if bf16 else torch.float32, act=nv.ACT_GELU_TANH)
     err = (got.double().cpu() - want).abs()
     assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("m", [1, 4])
+def test_output_beside_x(orc, m):
+    """x and y as parts of one buffer; over each other they are refused."""
+    q, w = _weights(orc, 256, 256, nv.SF_MMA128x4, 14)
+    wide = torch.randn(m, 768, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    before = wide.clone()
+    for at in (0, 512):
+        y = nv.gemv(wide[:, 256:512], q, out=wide[:, at:at + 256])
+        _check(y, before[:, 256:512], w, True)
+        assert torch.equal(wide[:, 256:512], before[:, 256:512])
+    wide.copy_(before)
+    for at in (8, 256, 504):
+        with pytest.raises(nv.NVFP4Error):
+            nv.gemv(wide[:, 256:512], q, out=wide[:, at:at + 256])
+    assert torch.equal(wide, before)

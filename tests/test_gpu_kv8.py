@@ -738,3 +738,24 @@ def test_plan_with_the_largest_slot_map(fits):
     for at in range(23, 2 ** 31 - 1, 1 << 28):
         assert bool((p.slot_map[at:at + (1 << 28)] == -1).all())
     assert nv.device_status() == (N.OK if fits else N.ERR_INVALID_ARG)
+
+
+@pytest.mark.parametrize("nq", [1, 5, 40])
+def test_output_beside_the_queries(nq):
+    """Queries and output as parts of one fused buffer: apart, though their spans meet."""
+    c = _random_cache(10, 16, 2, 64, 28)
+    wide = torch.randn(nq, 12, 64, generator=torch.Generator().manual_seed(2))
+    wide = wide.to(torch.bfloat16).cuda()
+    before = wide.clone()
+    args = (i32([0, nq]), i32([150]), i32([list(range(10))]))
+    want = c.attention(before[:, 2:6].contiguous(), *args, max_q=nq)
+    for at in (6, 8):
+        got = c.attention(wide[:, 2:6], *args, max_q=nq, out=wide[:, at:at + 4])
+        assert torch.equal(got, want)
+        keep = [h for h in range(12) if not at <= h < at + 4]
+        assert torch.equal(wide[:, keep], before[:, keep])
+        wide.copy_(before)
+    for at in (1, 3, 5):
+        with pytest.raises(nv.NVFP4Error):
+            c.attention(wide[:, 2:6], *args, max_q=nq, out=wide[:, at:at + 4])
+    assert torch.equal(wide, before)

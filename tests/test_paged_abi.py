@@ -263,3 +263,49 @@ def test_attention_rejects_tables_too_wide_for_its_look_ahead(L, page):
     for pages in (most + 1, 2 ** 31 // page - 1):
         assert _attention(L, _cache8(page=page), pages=pages, stride=pages, max_kv=2 ** 31 - 1) == \
             N.ERR_UNSUPPORTED_SHAPE
+
+
+G = 1 << 30   # buffers far apart
+
+
+def _apart(cols=1024, rows=1024, **kw):
+    """gemv arguments without an overlap: 4 rows, N = K."""
+    w = N.Tensor(FAKE + 2 * G, FAKE + 3 * G, FAKE + 4 * G, rows, cols, N.SF_MMA128x4)
+    return dict(dict(x=FAKE, m=4, ldx=cols, w=w, y=FAKE + G, ldy=rows), **kw)
+
+
+@pytest.mark.parametrize("y,ldy", [
+    (FAKE, 1024),                       # x itself
+    (FAKE + 2 * 1024 * 3, 1024),        # its last row
+    (FAKE - 2 * 1024, 1024), (FAKE - 2, 1024), (FAKE + 2, 2048),
+    (FAKE + 2 * G, 1024), (FAKE + 2 * G + 1024 * 512 - 2, 1024), (FAKE + 2 * G - 6146, 2048),
+    (FAKE + 3 * G + 1024 * 64 - 2, 1024), (FAKE + 4 * G, 1024), (FAKE + 4 * G - 8190, 1024)])
+def test_gemv_rejects_outputs_over_inputs(L, y, ldy):
+    assert _gemv(L, **_apart(y=y, ldy=ldy)) == N.ERR_INVALID_ARG
+
+
+def test_gemv_rejects_outputs_that_reach_into_the_next_row(L):
+    # x and y share rows of 2048: y begins in x's columns, or ends in the next row's
+    for at in (1022, 1026):
+        assert _gemv(L, **_apart(ldx=2048, ldy=2048, y=FAKE + 2 * at)) == N.ERR_INVALID_ARG
+    # one row each, of different strides
+    assert _gemv(L, **_apart(m=1, ldx=1024, ldy=4096, y=FAKE + 2046)) == N.ERR_INVALID_ARG
+
+
+def _apart8(**kw):
+    """attention arguments without an overlap: 6 tokens of 32 heads of 128."""
+    return dict(dict(q=FAKE, out=FAKE + G, cu=FAKE + 2 * G, lens=FAKE + 3 * G, table=FAKE + 4 * G,
+                     lse=FAKE + 5 * G, scratch=FAKE + 6 * G, ws=FAKE + 7 * G), **kw)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(out=FAKE), dict(out=FAKE + 16), dict(out=FAKE + 2 * 4096 * 5),
+    dict(qs=8192, os=8192, out=FAKE + 2 * 4088), dict(qs=8192, os=8192, out=FAKE + 2 * 4104),
+    dict(qs=8192, os=4096, out=FAKE + 2 * 4096), dict(lse=FAKE), dict(lse=FAKE + G + 2 * 4096 * 6 - 4),
+    dict(out=FAKE + 2 * G), dict(out=FAKE + 3 * G - 2 * 4096 * 6 + 16), dict(out=FAKE + 4 * G + 64),
+    dict(lse=FAKE + 4 * G + 79), dict(out=FAKE + 8 * G), dict(out=FAKE + 9 * G + 100 * 8 * 2048 - 16),
+    dict(lse=FAKE + 10 * G), dict(lse=FAKE + 11 * G + 100 * 8 * 4 - 4)])
+def test_attention_rejects_outputs_over_inputs(L, bad):
+    c = _cache8(k=FAKE + 8 * G, v=FAKE + 9 * G, ks=FAKE + 10 * G, vs=FAKE + 11 * G)
+    bad = {k: v - v % 4 if k == "lse" else v for k, v in bad.items()}
+    assert _attention(L, c, **_apart8(**bad)) == N.ERR_INVALID_ARG
