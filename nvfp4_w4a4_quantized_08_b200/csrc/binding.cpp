@@ -27,6 +27,8 @@
 namespace {
 
 struct Library {
+  decltype(&nvfp4_codes_bytes) codes_bytes;
+  decltype(&nvfp4_sf_bytes) sf_bytes;
   decltype(&nvfp4_gemv) gemv;
   decltype(&nvfp4_plan_pages) plan_pages;
   decltype(&nvfp4_kv8_append) append;
@@ -140,6 +142,23 @@ void count(Py_ssize_t have, Py_ssize_t want) {
   if (have != want) refuse(PyExc_TypeError, "wrong number of arguments");
 }
 
+// The buffers of an NVFP4 tensor of rows x cols, whose attributes are public.
+nvfp4_tensor weights(const at::Tensor& codes, const at::Tensor& sf, const at::Tensor& s_t,
+                     int64_t rows, int64_t cols, int32_t sf_layout) {
+  if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX)
+    refuse(PyExc_ValueError, "rows and cols of the weights must fit 31 bits");
+  for (const at::Tensor* t : {&codes, &sf})
+    if (t->scalar_type() != at::kByte || !t->is_contiguous())
+      refuse(PyExc_ValueError, "codes and sf of the weights must be contiguous uint8 tensors");
+  if (size_t(codes.numel()) < lib.codes_bytes(rows, cols) ||
+      size_t(sf.numel()) < lib.sf_bytes(rows, cols, sf_layout))
+    refuse(PyExc_ValueError, "codes or sf of the weights are too short for their rows and cols");
+  if (s_t.scalar_type() != at::kFloat || s_t.numel() != 1)
+    refuse(PyExc_ValueError, "s_t of the weights must be one fp32 element");
+  return {static_cast<uint8_t*>(codes.data_ptr()), static_cast<uint8_t*>(sf.data_ptr()),
+          static_cast<float*>(s_t.data_ptr()), rows, cols, sf_layout};
+}
+
 // ------------------------------------------------------------------ gemv
 // (x, codes, sf, s_t, rows, cols, sf_layout, out_dtype, out, act)
 PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -155,6 +174,7 @@ PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (x.device() != codes.device() || sf.device() != codes.device() ||
         s_t.device() != codes.device())
       refuse(PyExc_ValueError, "x and w must be on one device");
+    const nvfp4_tensor w = weights(codes, sf, s_t, rows, cols, int32(a[6], "sf_layout"));
     const int32_t x_code = dtype_code(x.scalar_type());
     at::Tensor out;
     if (a[8] != Py_None) {
@@ -175,10 +195,6 @@ PyObject* gemv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else
       refuse(PyExc_TypeError, "out_dtype must be a torch.dtype");
     const int32_t y_code = dtype_code(type), act = int32(a[9], "act");
-    const nvfp4_tensor w = {static_cast<uint8_t*>(codes.data_ptr()),
-                            static_cast<uint8_t*>(sf.data_ptr()),
-                            static_cast<float*>(s_t.data_ptr()), rows, cols,
-                            int32(a[6], "sf_layout")};
     nvfp4_status st;
     {
       const NoGil no_gil;
@@ -424,6 +440,8 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n) {
       f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(dlsym(h, name));
       if (!f) refuse(PyExc_ImportError, std::string("libnvfp4.so has no ") + name);
     };
+    get(lib.codes_bytes, "nvfp4_codes_bytes");
+    get(lib.sf_bytes, "nvfp4_sf_bytes");
     get(lib.gemv, "nvfp4_gemv");
     get(lib.plan_pages, "nvfp4_plan_pages");
     get(lib.append, "nvfp4_kv8_append");

@@ -309,3 +309,31 @@ def test_attention_rejects_outputs_over_inputs(L, bad):
     c = _cache8(k=FAKE + 8 * G, v=FAKE + 9 * G, ks=FAKE + 10 * G, vs=FAKE + 11 * G)
     bad = {k: v - v % 4 if k == "lse" else v for k, v in bad.items()}
     assert _attention(L, c, **_apart8(**bad)) == N.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("layout", [nv.SF_MMA128x4, nv.SF_ROWMAJOR])
+def test_gemv_checks_the_weights_buffers(layout):
+    """What the kernel would read past, or read wrongly, is refused by the binding."""
+    rows, cols = 200, 96
+    nb = nv.sf_bytes(rows, cols, layout)
+
+    def weights(**kw):
+        return nv.NVFP4Tensor(**{**dict(
+            codes=torch.zeros(rows, cols // 2, dtype=torch.uint8),
+            sf=torch.zeros(nb, dtype=torch.uint8), s_t=torch.zeros(1), rows=rows, cols=cols,
+            sf_layout=layout), **kw})
+    x = torch.zeros(1, cols)
+    u8 = torch.uint8
+    for bad in (dict(codes=torch.zeros(rows - 1, cols // 2, dtype=u8)),
+                dict(codes=torch.zeros(rows, cols, dtype=u8)[:, ::2]),
+                dict(codes=torch.zeros(cols // 2, rows, dtype=u8).t()),
+                dict(codes=torch.zeros(rows, cols // 2, dtype=torch.int8)),
+                dict(codes=torch.zeros(rows, cols // 2)),
+                dict(sf=torch.zeros(nb - 1, dtype=u8)), dict(sf=torch.zeros(2 * nb, dtype=u8)[::2]),
+                dict(sf=torch.zeros(nb, dtype=torch.int8)),
+                dict(s_t=torch.zeros(1, dtype=torch.float64)), dict(s_t=torch.zeros(0)),
+                dict(s_t=torch.zeros(2)), dict(rows=rows + 1), dict(rows=2 ** 31), dict(rows=-1)):
+        with pytest.raises(ValueError, match="of the weights"):
+            nv.gemv(x, weights(**bad))
+    with pytest.raises(ValueError, match="CUDA"):
+        nv.gemv(x, weights())
