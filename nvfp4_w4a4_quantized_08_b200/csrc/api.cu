@@ -634,8 +634,12 @@ nvfp4_status nvfp4_get_device_status(void* ws, void* stream) {
   uint32_t* dev_word = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + kWsStatus);
   if (cudaMemcpyAsync(&word, dev_word, sizeof(word), cudaMemcpyDeviceToHost, s) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  if (cudaMemsetAsync(dev_word, 0, sizeof(word), s) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return NVFP4_ERR_CUDA;
+  // cleared only where it is set: what another stream records in between is not lost
+  if (word != 0) {
+    if (cudaMemsetAsync(dev_word, 0, sizeof(word), s) != cudaSuccess) return NVFP4_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return NVFP4_ERR_CUDA;
+  }
   return static_cast<nvfp4_status>(word);
 }
 

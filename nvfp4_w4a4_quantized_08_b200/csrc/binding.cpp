@@ -8,6 +8,7 @@
 // refuses.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <dlfcn.h>
@@ -92,6 +93,14 @@ at::Tensor workspace(PyObject* ws, const at::Tensor& like, const On& on) {
     if (t.device() != like.device() || t.scalar_type() != at::kByte || !t.is_contiguous())
       refuse(PyExc_ValueError, "ws must be a contiguous uint8 tensor on the tensors' device");
     return t;
+  }
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
+    // a workspace apart from the stream's own
+    PyObject* t = PyObject_CallFunction(workspace_fn, "s", like.device().str().c_str());
+    if (!t) throw Refused();
+    const at::Tensor ws = THPVariable_Unpack(t);
+    Py_DECREF(t);
+    return ws;
   }
   // as long-lived as the streams: never freed, or it would be after the CUDA context
   static auto& known = *new std::map<std::pair<int, void*>, at::Tensor>;
@@ -269,6 +278,31 @@ PyObject* plan_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(slots));
     PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(head_out));
     return r;
+  })
+}
+
+// (bytes, device index) -> a uint8 tensor of zeros that belongs to no graph, also while the current
+// stream is being captured: allocated and filled on a stream that is not, and waited for.
+PyObject* zeros_outside_capture(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  NVFP4_CALL({
+    count(n, 2);
+    const int64_t bytes = integer(a[0]), index = integer(a[1]);
+    at::Tensor t;
+    {
+      const NoGil no_gil;
+      const auto device = static_cast<c10::DeviceIndex>(index);
+      const c10::cuda::CUDAStreamCaptureModeGuard relaxed(cudaStreamCaptureModeRelaxed);
+      for (int i = 0; i < 64 && !t.defined(); ++i) {   // more than the pool has
+        const c10::cuda::CUDAStream side = c10::cuda::getStreamFromPool(false, device);
+        const c10::cuda::CUDAStreamGuard guard(side);
+        if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+          continue;
+        t = at::zeros({bytes}, at::TensorOptions().dtype(at::kByte).device(at::kCUDA, device));
+        side.synchronize();
+      }
+    }
+    if (!t.defined()) refuse(PyExc_RuntimeError, "every stream is being captured");
+    return THPVariable_Wrap(t);
   })
 }
 
@@ -464,6 +498,7 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {method<init>("init"),
                          method<gemv>("gemv"),
                          method<plan_pages>("plan_pages"),
+                         method<zeros_outside_capture>("zeros_outside_capture"),
                          method<kv8_shape>("kv8_shape"),
                          method<kv8_append>("kv8_append"),
                          method<kv8_attention>("kv8_attention"),

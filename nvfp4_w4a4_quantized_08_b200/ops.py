@@ -26,20 +26,38 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 _workspaces: Dict[Tuple[int, int], torch.Tensor] = {}
+_captured_workspaces: Dict[Tuple[int, int], torch.Tensor] = {}
+
+
+def _capturing(idx: int) -> bool:
+    if idx == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(idx):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def workspace(device=None) -> torch.Tensor:
     """A zero-filled workspace for the current stream of `device` (cached).
-    Calls that share it must stay ordered on that stream."""
+    Calls that share it must stay ordered on that stream.
+
+    While the stream is being captured: a second one, which the graphs captured
+    on it share and which belongs to none of them.  device_status reads it too.
+    Graphs of one stream that are replayed at the same time need a `ws` of their
+    own, unless only the status word is used (plan_pages, KVCache8)."""
     idx = None if device is None else torch.device(device).index
     if idx is None:
         idx = torch.cuda.current_device()
     key = (idx, torch._C._cuda_getCurrentRawStream(idx))
-    ws = _workspaces.get(key)
+    captured = _capturing(idx)
+    known = _captured_workspaces if captured else _workspaces
+    ws = known.get(key)
     if ws is None:
-        ws = torch.zeros(N.lib().nvfp4_workspace_bytes(), dtype=torch.uint8,
-                         device=torch.device("cuda", idx))
-        _workspaces[key] = ws
+        nbytes = N.lib().nvfp4_workspace_bytes()
+        if captured:   # zeros made here would be a node of the graph, made again in each replay
+            ws = (_binding or _load_binding()).zeros_outside_capture(nbytes, idx)
+        else:
+            ws = torch.zeros(nbytes, dtype=torch.uint8, device=torch.device("cuda", idx))
+        known[key] = ws
     return ws
 
 
@@ -279,7 +297,8 @@ def plan_pages(cached_lens: torch.Tensor, new_lens: torch.Tensor, block_table: t
     """nvfp4_plan_pages: pages and slots for each request's new tokens, on the
     device.  block_table [batch, max_pages] is updated in place; the rest are
     new tensors (free_head of the result goes into the next call).  Lengths that
-    do not fit are reported by device_status, and then change nothing."""
+    do not fit are reported by device_status, also where a replayed graph meets
+    them, and then change nothing."""
     return PagePlan(*(_binding or _load_binding()).plan_pages(
         cached_lens, new_lens, block_table, free_pages, free_head, page_tokens, n_pages, max_new,
         ws))
@@ -377,9 +396,17 @@ class SinkPlan:
 
 def device_status(ws: Optional[torch.Tensor] = None) -> int:
     """nvfp4_get_device_status: sync the current stream, read and clear the
-    workspace status word."""
-    ws = workspace() if ws is None else ws
-    return int(N.lib().nvfp4_get_device_status(ws.data_ptr(), _stream()))
+    workspace status word.  Without `ws`: that of the current stream's workspace,
+    or where that is OK the first that is not of the workspaces of captured calls
+    on the current device, whichever stream their graphs were replayed on (wait
+    for the others first)."""
+    if ws is not None:
+        return int(N.lib().nvfp4_get_device_status(ws.data_ptr(), _stream()))
+    status = device_status(workspace())
+    for (idx, _), captured in list(_captured_workspaces.items()):
+        if status == N.OK and idx == torch.cuda.current_device():
+            status = device_status(captured)
+    return status
 
 
 def set_wait_limit_ns(ns: int) -> None:

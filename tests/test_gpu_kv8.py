@@ -759,3 +759,83 @@ def test_output_beside_the_queries(nq):
         with pytest.raises(nv.NVFP4Error):
             c.attention(wide[:, 2:6], *args, max_q=nq, out=wide[:, at:at + 4])
     assert torch.equal(wide, before)
+
+
+# ---------------------------------------------------------------- captured calls
+def _new_stream():
+    """A stream that no call has used: captures on it begin without a workspace."""
+    for _ in range(32):
+        s = torch.cuda.Stream(priority=-1)
+        if all(s.cuda_stream != key[1] for key in nv.ops._workspaces):
+            return s
+    pytest.skip("every stream of the pool has been used")
+
+
+def test_captured_calls_report_what_goes_wrong():
+    """The first calls on a stream are captured, in two graphs: device_status tells what went
+    wrong in a replay of either, whatever the other one did."""
+    s = _new_stream()
+    cached, new, head, table = i32([20]), i32([20]), i32([0]), i32([[0, 1, -1]])
+    frees = [i32([]), i32([2])]
+    graphs, plans = [], []
+    torch.cuda.synchronize()
+    for free in frees:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            plans.append(nv.plan_pages(cached, new, table, free, head, page_tokens=16, n_pages=8,
+                                       max_new=40))
+        graphs.append(g)
+    assert nv.device_status() == N.OK
+    for _ in range(2):
+        graphs[0].replay()
+        graphs[1].replay()
+        assert nv.device_status() == N.ERR_CAPACITY
+        assert nv.device_status() == N.OK
+        assert plans[0].seq_lens.tolist() == [20] and plans[1].seq_lens.tolist() == [40]
+        graphs[1].replay()
+        assert nv.device_status() == N.OK
+    new.fill_(-1)
+    graphs[1].replay()
+    graphs[0].replay()
+    assert nv.device_status() == N.ERR_INVALID_ARG
+    # the stream's own calls have a workspace apart from its graphs'
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        nv.plan_pages(i32([1]), i32([1]), table, frees[1], head, 16, 8, 4)
+        assert nv.device_status() == N.ERR_INVALID_ARG
+        assert nv.device_status() == N.OK
+
+
+def test_captured_workspaces_belong_to_no_graph():
+    """Two graphs of calls that need zeroed words, the first calls of their stream: the second is
+    replayed first, and after the other is gone."""
+    s = _new_stream()
+    x = [torch.randn(300, 512, generator=torch.Generator().manual_seed(i)).to(torch.bfloat16).cuda()
+         for i in range(2)]
+    want = [nv.quantize(t) for t in x]
+    got = [nv.ops.empty(300, 512) for _ in x]
+    graphs = []
+    torch.cuda.synchronize()
+    for t, out in zip(x, got):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            nv.quantize(t, out=out)
+        graphs.append(g)
+    ws = nv.ops._captured_workspaces[(0, s.cuda_stream)]
+    assert not ws.any()
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= ws.data_ptr() < seg["address"] + seg["total_size"]:
+            assert tuple(seg["segment_pool_id"]) == (0, 0)
+
+    def check(i):
+        got[i].codes.zero_(), got[i].sf.zero_(), got[i].s_t.zero_()
+        graphs[i].replay()
+        assert torch.equal(got[i].codes, want[i].codes) and torch.equal(got[i].sf, want[i].sf)
+        assert torch.equal(got[i].s_t, want[i].s_t)
+    for i in (1, 0, 1):
+        check(i)
+    graphs[0].reset()
+    graphs[0] = None
+    torch.cuda.empty_cache()
+    check(1)
