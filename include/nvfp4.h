@@ -429,6 +429,7 @@ NVFP4_API nvfp4_status nvfp4_kv8_append(const nvfp4_kv8_cache* cache, const void
  *   block_table: device [batch][table_stride], max_pages entries used a row, max_pages *
  *                page_tokens at most NVFP4_KV8_MAX_TOKENS (the kernels look some thousand
  *                tokens ahead in 32 bits)
+ *   batch:       1 to 65535
  *   max_q:       host, no request has more queries
  *   max_kv:      host, about the largest kv_lens: how the work is split goes by it, the
  *                result holds for any value >= 1 */

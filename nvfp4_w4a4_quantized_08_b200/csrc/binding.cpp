@@ -438,19 +438,21 @@ PyObject* kv8_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int want_lse = PyObject_IsTrue(a[13]);
     if (want_lse < 0) throw Refused();
     const at::Tensor ws = workspace(a[14], q, on);
-    nvfp4_status st;
+    nvfp4_status st = NVFP4_OK;
     {
       const NoGil no_gil;
       if (!out.defined()) out = at::empty({tokens, heads, d}, q.options());
       if (want_lse) lse = at::empty({tokens, heads}, q.options().dtype(at::kFloat));
-      const size_t need = lib.scratch_bytes(&c.c, &b, tokens, int32_t(heads), causal);
-      // a tensor of the call's own: calls on other streams and captured graphs share nothing
-      if (need) scratch = at::empty({int64_t(need)}, q.options().dtype(at::kByte));
-      st = lib.attention(&c.c, &b, q.data_ptr(), stride, tokens, int32_t(heads), causal, scale,
-                         out.data_ptr(), out_stride,
-                         want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
-                         need ? scratch.data_ptr() : nullptr, need, ws.data_ptr(),
-                         size_t(ws.numel()), on.stream);
+      if (batch > 0) {   // (no requests, as a plan may have them: no rows to write)
+        const size_t need = lib.scratch_bytes(&c.c, &b, tokens, int32_t(heads), causal);
+        // a tensor of the call's own: calls on other streams and captured graphs share nothing
+        if (need) scratch = at::empty({int64_t(need)}, q.options().dtype(at::kByte));
+        st = lib.attention(&c.c, &b, q.data_ptr(), stride, tokens, int32_t(heads), causal, scale,
+                           out.data_ptr(), out_stride,
+                           want_lse ? static_cast<float*>(lse.data_ptr()) : nullptr,
+                           need ? scratch.data_ptr() : nullptr, need, ws.data_ptr(),
+                           size_t(ws.numel()), on.stream);
+      }
     }
     check(st, "nvfp4_kv8_attention");
     if (!want_lse) return THPVariable_Wrap(out);

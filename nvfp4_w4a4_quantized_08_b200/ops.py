@@ -345,7 +345,7 @@ class KVCache8:
         q:         bf16 [tokens, q_heads, head_dim], the requests' queries packed;
                    q_heads a multiple of kv_heads.
         cu_q, seq_lens, block_table: int32 [batch + 1], [batch], [batch, pages] (a
-                   plan's cu_new and seq_lens).
+                   plan's cu_new and seq_lens; a batch of 0 writes nothing).
         max_q:     no request has more queries (default: all of q's tokens).
         max_kv:    about the longest request (default: the table's width); the
                    split of the work goes by it, not the result.

@@ -839,3 +839,17 @@ def test_captured_workspaces_belong_to_no_graph():
     graphs[0] = None
     torch.cuda.empty_cache()
     check(1)
+
+
+def test_no_requests_at_all():
+    """An idle step: a plan of no requests, and the attention over it."""
+    c = _random_cache(4, 16, 1, 64, 27)
+    none = i32([])
+    p = nv.plan_pages(none, none, none.view(0, 4), i32([1]), i32([0]), page_tokens=16, n_pages=4,
+                      max_new=3)
+    for tokens in (0, 3):   # (rows of no request are left)
+        q = torch.ones(tokens, 2, 64, dtype=torch.bfloat16, device="cuda")
+        out = torch.full_like(q, 5.0)
+        o, lse = c.attention(q, p.cu_new, p.seq_lens, none.view(0, 4), out=out, return_lse=True)
+        assert o is out and bool((out == 5).all()) and lse.shape == (tokens, 2)
+        assert c.attention(q, p.cu_new, p.seq_lens, none.view(0, 0)).shape == q.shape
