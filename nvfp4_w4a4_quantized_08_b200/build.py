@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -23,6 +24,22 @@ FLAGS = [
     # IEEE binary32: no flush-to-zero, correctly rounded division / sqrt
     "-ftz=false", "-prec-div=true", "-prec-sqrt=true",
 ]
+
+
+# Kernels whose warps share out their registers anew, which adds up only with this many a thread at
+# launch: a compiler that gives another number must not go unnoticed until the first call fails.
+LAUNCH_REGISTERS = {"chunk_kernel": 128}
+
+
+def check_registers(ptxas_log: str) -> None:
+    """Raises if a kernel of LAUNCH_REGISTERS is missing from the output of ptxas -v, or
+    uses another number of registers."""
+    found = re.findall(r"entry function '(\S+)'.*?Used (\d+) registers", ptxas_log, re.DOTALL)
+    for name, want in LAUNCH_REGISTERS.items():
+        used = {int(n) for symbol, n in found if name in symbol}
+        if used != {want}:
+            raise RuntimeError(f"{name} has to be compiled to {want} registers a thread, not "
+                               f"{sorted(used)}: its register split does not add up")
 
 
 def sources():
@@ -76,10 +93,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *FLAGS, "-shared", "-o", tmp, *sources()]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
+    cmd = [NVCC, "-Xptxas=-v", *FLAGS, "-shared", "-o", tmp, *sources()]
+    run = subprocess.run(cmd, stderr=subprocess.PIPE, text=True)
+    if verbose or run.returncode != 0 or "warning" in run.stderr:
+        sys.stderr.write(run.stderr)
+    run.check_returncode()
+    try:
+        check_registers(run.stderr)
+    except RuntimeError:
+        os.remove(tmp)
+        raise
     os.replace(tmp, LIB)
     return LIB
 

@@ -337,3 +337,20 @@ def test_gemv_checks_the_weights_buffers(layout):
             nv.gemv(x, weights(**bad))
     with pytest.raises(ValueError, match="CUDA"):
         nv.gemv(x, weights())
+
+
+def test_build_refuses_another_register_count():
+    """The many-row attention's register split holds for 128 registers a thread at launch."""
+    def log(*regs):
+        return "".join(
+            f"ptxas info    : Compiling entry function '_ZN5nvfp4{n}{i}' for 'sm_100a'\n"
+            f"ptxas info    : Function properties for _ZN5nvfp4{n}{i}\n"
+            "    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads\n"
+            f"ptxas info    : Used {r} registers, used 1 barriers\n"
+            for i, (n, r) in enumerate(regs))
+    both = ("12chunk_kernelILi64EE", 128), ("12chunk_kernelILi128EE", 128)
+    nbuild.check_registers(log(("11join_kernel", 40), *both, ("11gemv_kernel", 124)))
+    for bad in ([("12chunk_kernelILi64EE", 120), both[1]], [both[0], ("12chunk_kernelILi128EE", 168)],
+                [("11join_kernel", 128)], []):
+        with pytest.raises(RuntimeError, match="128 registers"):
+            nbuild.check_registers(log(*bad))
