@@ -88,8 +88,7 @@ def build_binding(force: bool = False) -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_binding(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
@@ -104,6 +103,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.remove(tmp)
         raise
     os.replace(tmp, LIB)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    build_library(force, verbose)   # first: it needs no Python or torch headers
+    build_binding(force)
     return LIB
 
 

@@ -1,6 +1,8 @@
 """Host-side refusals of the matrix-vector, page-plan and 8-bit cache entry points: every call
 has an invalid argument, so it returns before any device work."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -354,3 +356,20 @@ def test_build_refuses_another_register_count():
                 [("11join_kernel", 128)], []):
         with pytest.raises(RuntimeError, match="128 registers"):
             nbuild.check_registers(log(*bad))
+
+
+def test_library_is_built_without_the_binding(monkeypatch, tmp_path):
+    """No host compiler or no torch headers: the error comes after libnvfp4.so is there."""
+    monkeypatch.setattr(nbuild, "LIB", str(tmp_path / "libnvfp4.so"))
+    monkeypatch.setattr(nbuild, "BINDING", str(tmp_path / "_binding.so"))
+
+    def run(cmd, **kw):
+        if cmd[0] != nbuild.NVCC:
+            raise FileNotFoundError(cmd[0])
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, None, "entry function 'chunk_kernel' for "
+                                           "'sm_100a'\nptxas info    : Used 128 registers\n")
+    monkeypatch.setattr(nbuild.subprocess, "run", run)
+    with pytest.raises(FileNotFoundError):
+        nbuild.build()
+    assert os.listdir(tmp_path) == ["libnvfp4.so"]
