@@ -64,13 +64,19 @@ def up_to_date() -> bool:
 
 
 def build_binding(force: bool = False) -> str:
-    src = os.path.join(CSRC, "binding.cpp")
-    header = os.path.join(os.path.dirname(HERE), "include", "nvfp4.h")
-    if not force and _newer(BINDING, [src, header]):
-        return BINDING
     import sysconfig
 
     import torch
+
+    src = os.path.join(CSRC, "binding.cpp")
+    header = os.path.join(os.path.dirname(HERE), "include", "nvfp4.h")
+    # the C++ interfaces of torch and Python it is compiled against, noted beside it
+    built_for = f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}\n"
+    stamp = BINDING + ".torch"
+    if not force and _newer(BINDING, [src, header]) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == built_for:
+                return BINDING
     from torch.utils import cpp_extension
 
     lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -80,11 +86,14 @@ def build_binding(force: bool = False) -> str:
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           f'-DNVFP4_TORCH_VERSION="{torch.__version__}"',
            *[f"-isystem{i}" for i in includes], src, "-o", tmp, f"-L{lib_dir}",
            f"-Wl,-rpath,{lib_dir}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
            "-lc10_cuda", "-ldl"]
     subprocess.run(cmd, check=True)
     os.replace(tmp, BINDING)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return BINDING
 
 

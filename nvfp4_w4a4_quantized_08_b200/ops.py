@@ -268,6 +268,10 @@ def _load_binding():
     except ImportError as e:
         raise RuntimeError("the torch binding has not been built for this torch; run python -m "
                            f"nvfp4_w4a4_quantized_08_b200.build ({e})") from e
+    # (a binding for another torch may load all the same, and then call what is no longer there)
+    if b.torch_version != torch.__version__:
+        raise RuntimeError(f"the torch binding has been built for torch {b.torch_version}, not "
+                           f"{torch.__version__}; run python -m nvfp4_w4a4_quantized_08_b200.build")
     b.init(N.LIB_PATH, NVFP4Error, workspace)
     _binding = b
     return b

@@ -373,3 +373,24 @@ def test_library_is_built_without_the_binding(monkeypatch, tmp_path):
     with pytest.raises(FileNotFoundError):
         nbuild.build()
     assert os.listdir(tmp_path) == ["libnvfp4.so"]
+
+
+def test_binding_is_rebuilt_for_another_torch(L, monkeypatch, tmp_path):
+    monkeypatch.setattr(nbuild, "BINDING", str(tmp_path / "_binding.so"))
+    compiled = []
+
+    def run(cmd, **kw):
+        compiled.append([a for a in cmd if "TORCH_VERSION" in a])
+        open(cmd[cmd.index("-o") + 1], "w").close()
+    monkeypatch.setattr(nbuild.subprocess, "run", run)
+    nbuild.build_binding()
+    nbuild.build_binding()
+    assert len(compiled) == 1 and torch.__version__ in compiled[0][0]
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    nbuild.build_binding()
+    nbuild.build_binding()
+    assert compiled[1:] == [['-DNVFP4_TORCH_VERSION="1.0"']]
+    # and one that is there all the same is not called
+    monkeypatch.setattr(nv.ops, "_binding", None)
+    with pytest.raises(RuntimeError, match="not 1.0"):
+        nv.ops._load_binding()
