@@ -137,7 +137,7 @@ __device__ __forceinline__ void load_scores(uint32_t addr, uint32_t (&r)[4][32])
   regs_after_wait(r[3]);
 }
 
-template <int kD>
+template <int kD, bool kBrief>
 __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constant__ Args a) {
   using L = Layout<kD>;
   extern __shared__ uint8_t smem_raw[];
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   const uint32_t tmem = *tmem_ptr;
   pdl_wait();
   pdl_trigger();
-  const WarpWaiter waiter{{a.wait_limit_ns, abort_flag, a.status}};
+  const WarpWaiter<kBrief> waiter{{a.wait_limit_ns, abort_flag, a.status}};
 
   const Request rq = kv8::request(a, b, threadIdx.x == 0 && blockIdx.x == 0 && split == 0);
   const int rows = rq.nq * a.group, base = tile * kRows * kTiles;
@@ -608,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         return id < a.n_pages ? id : -1;
       };
       constexpr uint32_t kBytes = 16 * kD;   // of a group
-      int page = page_of(0), j = 0;
-      for (; j < n_tiles; ++j) {
+      int page = page_of(0), issued[2] = {0, 0};   // tiles whose K, V copies have begun
+      for (int j = 0; j < n_tiles; ++j) {
         const int next = page_of(j + 1);
         const uint32_t rs = j % L::kRaw, empty = ((j / L::kRaw) & 1) ^ 1;
         const int tok = t_begin + j * kKeys + 16 * lane;
@@ -640,18 +640,23 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
                 "l"((pl ? a.v_codes : a.k_codes) + at), "r"(kBytes), "r"(full)
                 : "memory");
           __syncwarp();
+          ++issued[pl];
         }
         if (!ok) break;
         page = next;
       }
-      // drain: every copy issued has landed before the CTA may leave (an abort may have come
-      // between a tile's K and V: its K is waited for, its V was not begun)
+      // drain: every copy issued has landed before the CTA may leave (a wait that ran out may have
+      // come between a tile's K and V)
+#pragma unroll
       for (int pl = 0; pl < 2; ++pl)
-        for (int d = max(0, j - L::kRaw); d < (pl == 0 ? min(j + 1, n_tiles) : j); ++d) {
+        for (int d = max(0, issued[pl] - L::kRaw); d < issued[pl]; ++d) {
           const uint32_t full = (pl ? bar_rv_full : bar_rk_full) + 8 * (d % L::kRaw);
           const uint64_t t0 = globaltimer();
           while (!bar_try_wait(full, (d / L::kRaw) & 1)) {
-            if (globaltimer() - t0 > 2000000000ull) break;
+            if (globaltimer() - t0 > 2000000000ull) {
+              record_status(a.status, NVFP4_ERR_TIMEOUT);
+              break;
+            }
           }
         }
     }
@@ -668,17 +673,24 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
   }
 }
 
-template <int kD>
+template <int kD, bool kBrief>
 cudaError_t launch(const Args& a, dim3 grid, cudaStream_t st) {
-  cudaError_t e = allow_smem<chunk_kernel<kD>>(Layout<kD>::kBytes);
+  cudaError_t e = allow_smem<chunk_kernel<kD, kBrief>>(Layout<kD>::kBytes);
   if (e != cudaSuccess) return e;
-  // the register split above adds up only with this launch allocation
+  // the register split above adds up only with this launch allocation (the build checks it too)
   static const int regs = [] {
     cudaFuncAttributes f = {};
-    return cudaFuncGetAttributes(&f, chunk_kernel<kD>) == cudaSuccess ? f.numRegs : 0;
+    return cudaFuncGetAttributes(&f, chunk_kernel<kD, kBrief>) == cudaSuccess ? f.numRegs : 0;
   }();
   if (regs != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return launch_pdl(chunk_kernel<kD>, grid, dim3(kThreads), size_t(Layout<kD>::kBytes), st, a);
+  return launch_pdl(chunk_kernel<kD, kBrief>, grid, dim3(kThreads), size_t(Layout<kD>::kBytes), st,
+                    a);
+}
+
+template <int kD>
+cudaError_t launch_dim(const Args& a, dim3 grid, cudaStream_t st) {
+  return a.wait_limit_ns < kBriefNs ? launch<kD, true>(a, grid, st)
+                                    : launch<kD, false>(a, grid, st);
 }
 
 }  // namespace kv8_chunk
@@ -687,7 +699,8 @@ cudaError_t launch_kv8_chunk(const kv8::Args& a, int32_t head_dim, int32_t row_t
                              cudaStream_t st) {
   const dim3 grid(unsigned(a.kv_heads) * unsigned(row_tiles), unsigned(batch),
                   unsigned(a.n_splits));
-  return head_dim == 64 ? kv8_chunk::launch<64>(a, grid, st) : kv8_chunk::launch<128>(a, grid, st);
+  return head_dim == 64 ? kv8_chunk::launch_dim<64>(a, grid, st)
+                        : kv8_chunk::launch_dim<128>(a, grid, st);
 }
 
 }  // namespace nvfp4

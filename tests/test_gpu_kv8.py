@@ -2,6 +2,7 @@
 scales) and the attention (tests/_kv8.py's bounds), alone and together."""
 import math
 import random
+import time
 
 import pytest
 import torch
@@ -853,3 +854,30 @@ def test_no_requests_at_all():
         o, lse = c.attention(q, p.cu_new, p.seq_lens, none.view(0, 4), out=out, return_lse=True)
         assert o is out and bool((out == 5).all()) and lse.shape == (tokens, 2)
         assert c.attention(q, p.cu_new, p.seq_lens, none.view(0, 0)).shape == q.shape
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_waits_that_run_out_report_and_recover(dim):
+    """The many-row kernel with a limit of 0 ns: a wait that finds its phase not over yet (the first
+    for the codes from memory, say) runs out.  The kernel records it, ends what it has in flight,
+    frees tensor memory and returns, soon; the next call with the normal limit is right."""
+    c = _random_cache(200, 16, 2, dim, 29)
+    q = torch.randn(700, 4, dim, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    q = q.cuda()
+    args = (q, i32([0, 400, 700]), i32([1500, 1700]),
+            i32([list(range(94)) + [0] * 13, list(range(93, 200))]))
+    good = c.attention(*args, max_q=400)
+    seen = []
+    for _ in range(4):
+        try:
+            nv.set_wait_limit_ns(0)
+            torch.cuda.synchronize()
+            began = time.monotonic()
+            c.attention(*args, max_q=400)
+            seen.append(nv.device_status())
+            assert time.monotonic() - began < 1.0   # (a drain that waits for nothing takes 2 s)
+        finally:
+            nv.set_wait_limit_ns(2_000_000_000)
+        assert torch.equal(c.attention(*args, max_q=400), good)
+        assert nv.device_status() == N.OK
+    assert all(st in (N.OK, N.ERR_TIMEOUT) for st in seen) and N.ERR_TIMEOUT in seen, seen
