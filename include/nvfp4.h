@@ -453,6 +453,7 @@ typedef struct {
  *   q:   device bf16, tq tokens at q_token_stride elements (>= q_heads * head_dim, a
  *        multiple of 8), q_heads x head_dim contiguous in a token; 16-byte aligned.
  *   q_heads: a multiple of kv_heads.
+ *   softmax_scale: above 0, and finite times log2(e).
  *   out: device bf16, same layout at out_token_stride, memory of its own (a row of q is read
  *        by several blocks; tokens beside those of q in one buffer, at one stride, are apart
  *        from them).  Rows of no request are left.

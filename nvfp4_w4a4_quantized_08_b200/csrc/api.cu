@@ -583,7 +583,8 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
   st = check_kv8_batch(cache, batch, tq, q_heads, causal);
   if (st != NVFP4_OK) return st;
   if (tq > 0 && (!q || !out)) return NVFP4_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.0f) || !std::isfinite(softmax_scale)) return NVFP4_ERR_INVALID_ARG;
+  const float scale_log2 = float(double(softmax_scale) * 1.4426950408889634);
+  if (!(softmax_scale > 0.0f) || !std::isfinite(scale_log2)) return NVFP4_ERR_INVALID_ARG;
   const int64_t row = int64_t(q_heads) * cache->head_dim;
   if (q_token_stride < row || out_token_stride < row) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || q_token_stride % 8 != 0 ||
@@ -620,7 +621,7 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
   d.out = out;
   d.out_stride = out_token_stride;
   d.lse = lse;
-  d.scale_log2 = float(double(softmax_scale) * 1.4426950408889634);
+  d.scale_log2 = scale_log2;
   d.scratch = scratch;
   d.ws = ws;
   d.wait_limit_ns = g_wait_limit_ns.load();

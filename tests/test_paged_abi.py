@@ -394,3 +394,9 @@ def test_binding_is_rebuilt_for_another_torch(L, monkeypatch, tmp_path):
     monkeypatch.setattr(nv.ops, "_binding", None)
     with pytest.raises(RuntimeError, match="not 1.0"):
         nv.ops._load_binding()
+
+
+@pytest.mark.parametrize("scale", [3e38, 2.4e38, -1e-9])
+def test_attention_rejects_scales_that_overflow_in_base_2(L, scale):
+    assert _attention(L, _cache8(k=FAKE + 8 * G, v=FAKE + 9 * G, ks=FAKE + 10 * G,
+                                 vs=FAKE + 11 * G), **_apart8(scale=scale)) == N.ERR_INVALID_ARG
