@@ -29,13 +29,6 @@ _workspaces: Dict[Tuple[int, int], torch.Tensor] = {}
 _captured_workspaces: Dict[Tuple[int, int], torch.Tensor] = {}
 
 
-def _capturing(idx: int) -> bool:
-    if idx == torch.cuda.current_device():
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.device(idx):
-        return torch.cuda.is_current_stream_capturing()
-
-
 def workspace(device=None) -> torch.Tensor:
     """A zero-filled workspace for the current stream of `device` (cached).
     Calls that share it must stay ordered on that stream.
@@ -45,10 +38,15 @@ def workspace(device=None) -> torch.Tensor:
     Graphs of one stream that are replayed at the same time need a `ws` of their
     own, unless only the status word is used (plan_pages, KVCache8)."""
     idx = None if device is None else torch.device(device).index
+    current = torch.cuda.current_device() if idx is None else torch._C._cuda_getDevice()
     if idx is None:
-        idx = torch.cuda.current_device()
+        idx = current
     key = (idx, torch._C._cuda_getCurrentRawStream(idx))
-    captured = _capturing(idx)
+    if idx == current:
+        captured = torch._C._cuda_isCurrentStreamCapturing()
+    else:
+        with torch.cuda.device(idx):
+            captured = torch._C._cuda_isCurrentStreamCapturing()
     known = _captured_workspaces if captured else _workspaces
     ws = known.get(key)
     if ws is None:
