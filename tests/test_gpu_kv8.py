@@ -881,3 +881,55 @@ def test_waits_that_run_out_report_and_recover(dim):
         assert torch.equal(c.attention(*args, max_q=400), good)
         assert nv.device_status() == N.OK
     assert all(st in (N.OK, N.ERR_TIMEOUT) for st in seen) and N.ERR_TIMEOUT in seen, seen
+
+
+# ---------------------------------------------------------------- both planes, step by step
+@pytest.mark.parametrize("heads,dim", [(24, 64), (8, 128)])
+def test_append_many_single_tokens_both_planes(heads, dim):
+    """K and V of their own (not one the other's negative) in pages that hold tokens already."""
+    page, batch = 16, 3000
+    c = _random_cache(batch, page, heads, dim, 30)
+    slots = [p * page + (7 * p) % page for p in range(batch)]
+    before = _planes64(c)
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(batch, heads, dim, generator=g).mul_(torch.exp2(
+        torch.randint(-6, 7, (batch, 1, 1), generator=g).float())) for _ in range(2))
+    k, v = k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda()
+    c.append(k, v, i32(slots))
+    keep = list(range(0, batch, 97))   # a page is one run here, and goes by itself
+    sub = [t[keep] for t in before]
+    for x, value, scale in ((k, sub[0], sub[2]), (v, sub[1], sub[3])):
+        ref.append(x.cpu().double()[keep], value, scale, [i * page + slots[p] % page
+                                                          for i, p in enumerate(keep)], page)
+    for got, want in zip(_planes64(c), sub):
+        assert torch.equal(got[keep], want)
+
+
+@pytest.mark.parametrize("page,dim,hkv,hq", [(16, 128, 2, 8), (32, 64, 1, 4), (48, 64, 3, 3)])
+def test_serving_steps_fill_the_cache(page, dim, hkv, hq):
+    """Plans and appends step after step, with an attention between that must change nothing: the
+    tables, lengths, codes and scales of K and V are the plain forms' after every step."""
+    cache = nv.KVCache8.empty(40, page, hkv, dim)
+    steps = [[30, 1, 0, 77], [1, 1, 50, 1], [1, 0, 1, 1], [1, 3, 1, 20], [0, 0, 0, 0], [1, 1, 1, 1]]
+    g = torch.Generator().manual_seed(6)
+    order = torch.randperm(40, generator=g).tolist()
+    free, head, cached = i32(order), i32([0]), i32([0] * 4)
+    table = torch.full((4, 12), -1, dtype=torch.int32, device="cuda")
+    rows, taken, lens = table.tolist(), 0, [0] * 4
+    for new in steps:
+        tokens = sum(new)
+        qkv = torch.randn(tokens + 5, hq + 2 * hkv, dim, generator=g)
+        qkv *= torch.exp2(torch.randint(-6, 7, (tokens + 5, 1, 1), generator=g).float())
+        qkv = qkv.to(torch.bfloat16).cuda()
+        before = _planes64(cache)
+        p = nv.plan_pages(cached, i32(new), table, free, head, page_tokens=page, n_pages=40,
+                          max_new=tokens + 5)
+        lens, cu, slots, rows, taken = ref.plan(lens, new, rows, order, taken, page)
+        k, v = qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+        cache.append(k, v, p.slot_map)
+        cache.attention(qkv[:, :hq], p.cu_new, p.seq_lens, table, max_q=max(max(new), 1))
+        assert p.seq_lens.tolist() == lens and p.cu_new.tolist() == cu
+        assert p.slot_map.tolist() == slots + [-1] * 5
+        assert table.tolist() == rows and p.free_head.tolist() == [taken]
+        _check_append(cache, k, v, slots + [-1] * 5, before)
+        cached, head = p.seq_lens, p.free_head
