@@ -1,5 +1,6 @@
 """GPU parity of the paged 8-bit cache: page plans (exact), the quantizing write (exact codes and
 scales) and the attention (tests/_kv8.py's bounds), alone and together."""
+import contextlib
 import math
 import random
 import time
@@ -933,3 +934,51 @@ def test_serving_steps_fill_the_cache(page, dim, hkv, hq):
         assert table.tolist() == rows and p.free_head.tolist() == [taken]
         _check_append(cache, k, v, slots + [-1] * 5, before)
         cached, head = p.seq_lens, p.free_head
+
+
+@pytest.mark.parametrize("steps,batch,dim,hkv,hq,page,prompt", [
+    (60, 1, 128, 2, 8, 16, 37), (60, 3, 64, 2, 6, 16, 100), (40, 16, 128, 4, 16, 32, 300),
+    (20, 2, 128, 8, 32, 64, 6000)])
+def test_a_chain_of_steps_in_one_graph(steps, batch, dim, hkv, hq, page, prompt):
+    """Each step's tokens come from the last step's output through a layer, its lengths and pages
+    from the last step's plan, and every call starts while the one before ends: the same bits as with
+    a wait after every call."""
+    width = -(-(prompt + steps) // page)
+    n_pages = batch * (width + 1)
+
+    def run(between, captured):
+        g = torch.Generator().manual_seed(5)
+        cache = nv.KVCache8.empty(n_pages, page, hkv, dim)
+        w = nv.quantize((torch.randn((hq + 2 * hkv) * dim, hq * dim, generator=g) * 0.05)
+                        .to(torch.bfloat16).cuda())
+        table = torch.full((batch, width), -1, dtype=torch.int32, device="cuda")
+        free, one = torch.randperm(n_pages, generator=g).int().cuda(), i32([1] * batch)
+        x = torch.randn(batch, hq * dim, generator=g).to(torch.bfloat16).cuda()
+        qkv = torch.randn(batch * prompt, hq + 2 * hkv, dim, generator=g).to(torch.bfloat16).cuda()
+        p = nv.plan_pages(i32([0] * batch), i32([prompt] * batch), table, free, i32([0]), page,
+                          n_pages, batch * prompt)
+        cache.append(qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], p.slot_map)
+        outs = [cache.attention(qkv[:, :hq], p.cu_new, p.seq_lens, table, max_q=prompt)]
+        graph = torch.cuda.CUDAGraph() if captured else None
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph) if captured else contextlib.nullcontext():
+            for _ in range(steps):
+                qkv = nv.gemv(x, w).view(batch, hq + 2 * hkv, dim)
+                between()
+                p = nv.plan_pages(p.seq_lens, one, table, free, p.free_head, page, n_pages, batch)
+                between()
+                cache.append(qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], p.slot_map)
+                between()
+                outs.append(cache.attention(qkv[:, :hq], p.cu_new, p.seq_lens, table, max_q=1))
+                between()
+                x = outs[-1].view(batch, hq * dim)
+        if captured:
+            graph.replay()
+        torch.cuda.synchronize()
+        return [*outs, table, cache.k_codes.view(torch.uint8), cache.v_codes.view(torch.uint8),
+                cache.k_scale, cache.v_scale], graph
+    want, _ = run(torch.cuda.synchronize, False)
+    for captured in (False, True):
+        got, graph = run(lambda: None, captured)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
