@@ -327,7 +327,8 @@ NVFP4_API int64_t nvfp4_sink_plan_frame_of_slot(const nvfp4_sink_plan* plan, int
 /* Matrix-vector products with NVFP4 weights: the linear layer of a few rows, whose
  * activations are not quantized,
  *   y[m][n] = act(s_t * sum_k x[m][k] v(q[n][k]) s_b[n][k/16])
- * Products are exact up to the representation of x (below), sums fp32.
+ * Products are exact up to the representation of x (below), sums fp32 (the one before its
+ * product with s_t has to fit them: s_t may be small).
  *   x:   device, bf16 or fp32 (x_dtype), m rows of W->cols values at stride ldx
  *        elements, 1 <= m <= NVFP4_GEMV_MAX_ROWS; 16-byte aligned, ldx * element size
  *        a multiple of 16 bytes.  Each row is taken, per 256 columns, relative to the
@@ -449,7 +450,7 @@ typedef struct {
  * over the tokens j of t's request, K and V head h / (q_heads / kv_heads).  causal != 0:
  * the queries are the request's last tokens, query i sees the first kv_len - n + 1 + i.
  * A row that sees nothing is 0 and its log-sum-exp -inf.  Scores, sums and the
- * normaliser in fp32; probabilities enter the product with V in 16 bits.
+ * normaliser in fp32; probabilities enter the product with V as fp16 (2^-11 of each).
  *   q:   device bf16, tq tokens at q_token_stride elements (>= q_heads * head_dim, a
  *        multiple of 8), q_heads x head_dim contiguous in a token; 16-byte aligned.
  *   q_heads: a multiple of kv_heads.

@@ -26,20 +26,22 @@
 // whole line, of each row, copied asynchronously into a ring of its own two steps deep.  (Loads
 // straight into registers, 64 bytes of a row at a time and 16 rows a warp, took 17.4 us for
 // 14336 x 4096 and one row, 13.7 with 32 rows; the rings took 11.5 at first.  Three steps deep
-// leaves one CTA an SM: 17 us.)  A CTA has 8 warps: KW of them split the columns (steps dealt out in turn), the
-// other factor 8 / KW takes further rows, which then share the converted x; KW falls with the
-// rows of x, so that the conversion stays a small part of the work.  For one or two rows a warp
-// converts what it reads itself, and no barrier is needed (14336 x 4096: 10.5 us against 11.3).  (Converting all of x first, in
-// a prologue, cost 0.7 us at 1024 x 1024.)  The 16 weight rows of a product are 4 i-values by
-// 4 rows 32 apart: the scale tile of the tensor-core layout keeps their scales in 64
-// contiguous bytes.  Where rows alone leave SMs idle, a cluster of up to 8 CTAs splits the
-// columns again; each CTA stores its sums to the one that finishes them, which adds them in
-// rank order: no workspace, no atomics, the same result every time.  (Fetching the others' sums
-// instead took 2 us a CTA of the cluster: 7 x 5000 x 14336 in clusters of 6 37 us against 23.)
+// leaves one CTA an SM: 17 us.)  A CTA has 8 warps: KW of them split the columns (steps dealt out
+// in turn), the other factor 8 / KW takes further rows, which then share the converted x; KW falls
+// with the rows of x, so that the conversion stays a small part of the work.  For one or two rows
+// a warp converts what it reads itself, and no barrier is needed (14336 x 4096: 10.5 us against
+// 11.3).  (Converting all of x first, in a prologue, cost 0.7 us at 1024 x 1024.)  The 16 weight
+// rows of a product are 4 i-values by 4 rows 32 apart: the scale tile of the tensor-core layout
+// keeps their scales in 64 contiguous bytes.  Where rows alone leave SMs idle, a cluster of up to
+// 8 CTAs splits the columns again; each CTA stores its sums to the one that finishes them, which
+// adds them in rank order: no workspace, no atomics, the same result every time.  (Fetching the
+// others' sums instead took 2 us a CTA of the cluster: 7 x 5000 x 14336 in clusters of 6 37 us
+// against 23.)
 //
-// 1 x 1024 x 1024 2.6 us (the launch, one step, the join of the warps); 1 x 14336 x 4096 10.5 us,
-// 48% of the copy rate; 7 x 5000 x 14336 in fp32 22 us, 29%, the conversions' and products'
-// latency with 16 warps an SM.
+// 1 x 1024 x 1024 2.1 us (the launch, one step, the join of the warps); 1 x 14336 x 4096 with its
+// GELU 10.7 us, 47% of the copy rate: 224 CTAs, so that half of the SMs have two and half one, and
+// 12 to 16 warps an SM (issue slots 47% in use); 7 x 5000 x 14336 in fp32 21.5 us, 29%, the
+// conversions' and products' latency with 16 warps an SM.
 #include <algorithm>
 
 #include "common.cuh"
@@ -116,8 +118,8 @@ __device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
 }
 
 __device__ __forceinline__ float gelu_tanh(float y) {
-  // y (1 + tanh u) / 2 = y / (1 + exp(-2u)), without the cancellation for y below 0 (there 1 + tanh u
-  // has no more than the last bits of 1); exp overflows to inf where the result is -0
+  // y (1 + tanh u) / 2 = y / (1 + exp(-2u)), without the cancellation for y below 0 (there
+  // 1 + tanh u has no more than the last bits of 1); exp overflows to inf where the result is -0
   const float u = 0.7978845608028654f * (y + 0.044715f * y * y * y);
   return y / (1.0f + expf(-2.0f * u));
 }
@@ -199,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
-          copy16(to[j] + stage + t * 16 * (kStep / 2), a.codes + 16 * int64_t(from[4 * t + j] + at), in);
+          copy16(to[j] + stage + t * 16 * (kStep / 2),
+                 a.codes + 16 * int64_t(from[4 * t + j] + at), in);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -308,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(const Args a) {
       // columns 64 c + 8 q .. of a step (lane 8 c + q): unit 4 q + c of its row, so that the
       // reads below, lanes c of one q, are 64 contiguous bytes
       const int pair = (SELF ? warp : step_of) * a.M + m;
-      uint8_t* d = xs + (buf * kPairs + pair) * kParts * kXRow + ((lane & 7) * 4 + (lane >> 3)) * 16;
+      uint8_t* d = xs + (buf * kPairs + pair) * kParts * kXRow +
+                   ((lane & 7) * 4 + (lane >> 3)) * 16;
       *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
       if constexpr (FP32)
         *reinterpret_cast<uint4*>(d + kXRow) = make_uint4(lo[0], lo[1], lo[2], lo[3]);

@@ -26,11 +26,12 @@
 // reference in use, and only where a sum of 16 of them shows that one might be too large for
 // fp16 is the tile taken again, in a slower form that finds the maximum and raises the
 // reference.  2640 rows over 10560 tokens and 24 heads: 429 us with the maximum taken every
-// time, 375 without (913 TFLOP/s, 55% of the measured bf16 burst; 269 with no exponentials
-// and no decoding at all).  On the way there: 624 us with S and P in one place and one MMA
-// warp; 456 with rings of their own for K and V; what did not help: sixteen softmax warps
-// of half a row each (517), a quarter of the exponentials as polynomials on the FMA pipe
-// (478 against 458), and warps that take turns at the exponentials (493 against 458).
+// time, 375 without; 269 with no exponentials and no decoding at all.  On the way there: 624 us
+// with S and P in one place and one MMA warp; 456 with rings of their own for K and V; what did
+// not help: sixteen softmax warps of half a row each (517), a quarter of the exponentials as
+// polynomials on the FMA pipe (478 against 458), and warps that take turns at the exponentials
+// (493 against 458).  These are single short graphs, before the card is at its power limit; over a
+// second of calls it is 390 us (879 TFLOP/s, 53% of the measured bf16 burst).
 //
 // The codes go into the products without their page scales.  Q is scaled by a power of two
 // per row to fp16 (largest element in [2^8, 2^9): exact for elements within 2^-22 of it, an
@@ -61,7 +62,7 @@ constexpr int kGroups = kKeys / 16;        // groups of tokens that share a page
 constexpr int kSoftWarps = 8;              // warps 0..7
 constexpr int kDecWarps = 4;               // warps 8..11
 constexpr int kMmaWarp = kSoftWarps + kDecWarps;
-constexpr int kThreads = 512;              // four warpgroups; the last has the MMA warp only
+constexpr int kThreads = 512;              // four warpgroups; the last: MMA of S, loads, MMA of P V
 constexpr int kLoadWarp = kMmaWarp + 1, kPvWarp = kMmaWarp + 2;
 constexpr int kStages = 2;                 // decoded tiles of K, and of V
 constexpr int kMetaStages = 4;             // page scales: read later than K
@@ -80,7 +81,7 @@ constexpr float kWide = 28.0f;    // |log2 s_v| above which a tile takes the slo
 template <int kD>
 struct Layout {
   static constexpr int kChunks = kD / 64;
-  static constexpr int kOp = kChunks * kChunkBytes;        // 128 rows x kD bf16
+  static constexpr int kOp = kChunks * kChunkBytes;        // 128 rows x kD fp16
   static constexpr int kQ = 0, kK = kTiles * kOp, kV = kK + kStages * kOp;
   static constexpr int kRaw = kD == 64 ? 3 : 1;            // tiles of codes ahead
   static constexpr int kRawBytes = kKeys * kD;             // of one plane
@@ -268,8 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) bar_arrive(bar_q + 8 * g);
       for (int j = 0; j < n_tiles; ++j) {
-        ok = waiter.wait(bar_meta + 8 * (j % kMetaStages),
-                                                 (j / kMetaStages) & 1);
+        ok = waiter.wait(bar_meta + 8 * (j % kMetaStages), (j / kMetaStages) & 1);
         if (!ok) break;
         // per group: K scale times scale * log2 e; log2 of the V scale; 1 / V scale (0: no
         // page, left out, with a log2 of -inf)
@@ -353,9 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
           float factor = 1.0f;
           if (mx - kBias > ref + kLazy || !seen) {
             if (mx > -INFINITY) {
-              // In two steps: the reference may rise by more than 2^126 through the pages' V scales
-              // alone, after tokens that still are most of the normaliser (O in units of the largest
-              // weight is lost then, the normaliser is not).
+              // In two steps: the reference may rise by more than 2^126 through the pages' V
+              // scales alone, after tokens that still are most of the normaliser (O in units of
+              // the largest weight is lost then, the normaliser is not).
               const float half = seen ? exp2_approx(0.5f * (ref - (mx - kBias))) : 0.0f;
               factor = half * half;
               ref = mx - kBias;
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t bar_raw = (pl ? bar_rv_full : bar_rk_full) + 8 * rs;
         const uint32_t bar_raw_empty = (pl ? bar_rv_empty : bar_rk_empty) + 8 * rs;
         ok = waiter.wait(bar_empty, empty) && waiter.wait(bar_raw, full);
-                if (!ok) break;
+        if (!ok) break;
         const uint32_t raw = sbase + (pl ? L::kRawV : L::kRawK) + rs * L::kRawBytes + t * 16;
         const uint32_t op = sbase + (pl ? L::kV : L::kK) + st * L::kOp;
 #pragma unroll 1
@@ -614,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(const __grid_constan
         const uint32_t rs = j % L::kRaw, empty = ((j / L::kRaw) & 1) ^ 1;
         const int tok = t_begin + j * kKeys + 16 * lane;
         const int in_page = tok - int(fast_div(a.page_div, uint32_t(tok))) * a.page_tokens;
-        const int64_t at = ((int64_t(max(page, 0)) * a.kv_heads + h) * a.page_tokens + in_page) * kD;
+        const int64_t at =
+            ((int64_t(max(page, 0)) * a.kv_heads + h) * a.page_tokens + in_page) * kD;
         const uint32_t have = __ballot_sync(0xFFFFFFFFu, page >= 0);
         bool ok = true;
 #pragma unroll

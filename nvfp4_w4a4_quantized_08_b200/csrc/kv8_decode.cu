@@ -89,7 +89,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int kLeft>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
@@ -721,14 +723,17 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   p.rows = p.chunked ? 256 : rows <= 8 ? 8 : 16;
   p.row_tiles = int32_t((rows + p.rows - 1) / p.rows);
   // Ranges, none shorter than 128 tokens.  Few units: as many as fill one wave of three CTAs
-  // an SM (2 x 131072 tokens, 8 heads: 86 us; 93 for four an SM, 107 in 2.7 waves), or the 8
+  // an SM (2 x 131072 tokens, 8 heads: 86 us; 93 for four an SM, 107 in 2.7 waves; short graphs:
+  // over a second of calls the 86 are 97, at the card's power limit), or the 8
   // of a cluster where that keeps a range below 512 tokens (1500 tokens, 24 heads: 6.3 us
   // against 8.3).  Many units: enough ranges for three waves of four CTAs an SM, because
   // lengths differ (64 ragged requests, 8 heads: 90 us in four ranges, 96 in two, 105 in one),
   // until there are two waves of units (200 requests: 76 us whole, 80 in two ranges).
   const int64_t units = int64_t(d.batch) * d.kv_heads * p.row_tiles;
   const int64_t sms = d.sm_count, wave = sms * 3;
-  int64_t n = units * 2 <= wave ? wave / units : units < sms * 8 ? (sms * 12 + units - 1) / units : 1;
+  int64_t n = units * 2 <= wave  ? wave / units
+              : units < sms * 8 ? (sms * 12 + units - 1) / units
+                                : 1;
   n = std::min(n, (int64_t(d.max_kv) + 127) / 128);
   if (n > kv8::kMaxCluster && d.max_kv <= kv8::kMaxCluster * 512) n = kv8::kMaxCluster;
   // Chunks: ranges only where the row tiles leave half of the SMs without a CTA.
@@ -743,7 +748,8 @@ Kv8Plan kv8_plan(const LaunchKv8Attn& d) {
   // In one wave the ranges of a unit can be a cluster, which joins them without a second
   // kernel (777 tokens, 24 heads: 5.4 us against 7.6); in several, CTAs that wait for their
   // cluster hold up others (64 ragged requests: 121 us against 94).
-  p.cluster = !p.chunked && p.n_splits > 1 && p.n_splits <= kv8::kMaxCluster && units * p.n_splits <= wave;
+  p.cluster = !p.chunked && p.n_splits > 1 && p.n_splits <= kv8::kMaxCluster &&
+              units * p.n_splits <= wave;
   p.scratch = p.n_splits == 1 || p.cluster
                   ? 0
                   : size_t(p.n_splits) * size_t(d.tq) * size_t(d.q_heads) *

@@ -1,5 +1,5 @@
 // tc.cuh -- what the attention kernels share of the sm_100a tensor core: barriers, tensor
-// memory, bf16 tcgen05.mma on 128-byte-swizzled operands, bounded waits.
+// memory, 16-bit tcgen05.mma on 128-byte-swizzled operands, bounded waits.
 #pragma once
 #include <utility>
 
@@ -8,7 +8,7 @@
 namespace nvfp4 {
 namespace tc {
 
-constexpr int kChunkBytes = 128 * 128;    // 128 rows x 64 bf16 (one K chunk of an operand)
+constexpr int kChunkBytes = 128 * 128;    // 128 rows x 64 of 16 bits (one K chunk of an operand)
 
 // ---------------------------------------------------------------- PTX wrappers
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -223,7 +223,7 @@ __device__ __forceinline__ void unrolled(F&& f, std::integer_sequence<uint32_t, 
 }
 
 // Byte offset of 16-byte unit u (0..15: elements 8u..8u+7) of row r in a
-// 128-row operand tile of 128 bf16 per row, in the tensor core's K-major,
+// 128-row operand tile of 128 16-bit elements per row, in the tensor core's K-major,
 // 128-byte-swizzled layout (two 64-element chunks of 16 KB).
 __device__ __forceinline__ uint32_t op_offset(uint32_t r, uint32_t u) {
   return (u >> 3) * kChunkBytes + (r >> 3) * 1024 + (r & 7) * 128 + (((u & 7) ^ (r & 7)) << 4);

@@ -348,7 +348,10 @@ class KVCache8:
                    q_heads a multiple of kv_heads.
         cu_q, seq_lens, block_table: int32 [batch + 1], [batch], [batch, pages] (a
                    plan's cu_new and seq_lens; a batch of 0 writes nothing).
-        max_q:     no request has more queries (default: all of q's tokens).
+        max_q:     no request has more queries (default: all of q's tokens).  Worth
+                   giving: up to 32 query rows (max_q * q_heads / kv_heads) a
+                   request take the kernel for single tokens, more the one for
+                   chunks, whose tiles have 256 rows.
         max_kv:    about the longest request (default: the table's width); the
                    split of the work goes by it, not the result.
         causal:    the queries are the requests' last tokens and see no later one.

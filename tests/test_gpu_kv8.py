@@ -941,8 +941,8 @@ def test_serving_steps_fill_the_cache(page, dim, hkv, hq):
     (20, 2, 128, 8, 32, 64, 6000)])
 def test_a_chain_of_steps_in_one_graph(steps, batch, dim, hkv, hq, page, prompt):
     """Each step's tokens come from the last step's output through a layer, its lengths and pages
-    from the last step's plan, and every call starts while the one before ends: the same bits as with
-    a wait after every call."""
+    from the last step's plan, and every call starts while the one before ends: the same bits as
+    with a wait after every call."""
     width = -(-(prompt + steps) // page)
     n_pages = batch * (width + 1)
 
