@@ -267,8 +267,9 @@ def _load_binding():
         raise RuntimeError("the torch binding has not been built for this torch; run python -m "
                            f"nvfp4_w4a4_quantized_08_b200.build ({e})") from e
     # (a binding for another torch may load all the same, and then call what is no longer there)
-    if b.torch_version != torch.__version__:
-        raise RuntimeError(f"the torch binding has been built for torch {b.torch_version}, not "
+    built_for = getattr(b, "torch_version", "of no known version")
+    if built_for != torch.__version__:
+        raise RuntimeError(f"the torch binding has been built for torch {built_for}, not "
                            f"{torch.__version__}; run python -m nvfp4_w4a4_quantized_08_b200.build")
     b.init(N.LIB_PATH, NVFP4Error, workspace)
     _binding = b
@@ -310,7 +311,9 @@ class KVCache8:
     """The paged 8-bit KV cache of one layer: E4M3 codes [n_pages, kv_heads,
     page_tokens, head_dim] and a power-of-two scale [n_pages, kv_heads] for K and
     for V.  A page holds page_tokens consecutive tokens of one request; which
-    page is whose is the callers' (plan_pages keeps block tables)."""
+    page is whose is the callers' (plan_pages keeps block tables).  Slots, pages
+    and lengths outside the buffers, and values that are not finite, are reported
+    by device_status, also where a replayed graph meets them."""
 
     def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor):
