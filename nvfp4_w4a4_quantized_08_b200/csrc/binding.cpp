@@ -46,6 +46,10 @@ struct Refused {};                     // a Python error is set
   throw Refused();
 }
 
+void initialised() {
+  if (!error_class) refuse(PyExc_RuntimeError, "init has not been called");
+}
+
 void check(nvfp4_status st, const char* what) {
   if (st == NVFP4_OK) return;
   PyObject* e = PyObject_CallFunction(error_class, "is", int(st), what);
@@ -79,7 +83,7 @@ struct On {
   c10::cuda::OptionalCUDAGuard guard;
   void* stream;
   On(const at::Tensor& t, const char* what) {
-    if (!error_class) refuse(PyExc_RuntimeError, "init has not been called");
+    initialised();
     if (!t.is_cuda()) refuse(PyExc_ValueError, std::string(what) + " takes CUDA tensors");
     if (t.get_device() != c10::cuda::current_device()) guard.set_index(t.get_device());
     stream = c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
@@ -154,6 +158,7 @@ void count(Py_ssize_t have, Py_ssize_t want) {
 // The buffers of an NVFP4 tensor of rows x cols, whose attributes are public.
 nvfp4_tensor weights(const at::Tensor& codes, const at::Tensor& sf, const at::Tensor& s_t,
                      int64_t rows, int64_t cols, int32_t sf_layout) {
+  initialised();
   if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX)
     refuse(PyExc_ValueError, "rows and cols of the weights must fit 31 bits");
   for (const at::Tensor* t : {&codes, &sf})

@@ -3,6 +3,7 @@ has an invalid argument, so it returns before any device work."""
 import ctypes
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
@@ -401,3 +402,18 @@ def test_binding_is_rebuilt_for_another_torch(L, monkeypatch, tmp_path):
 def test_attention_rejects_scales_that_overflow_in_base_2(L, scale):
     assert _attention(L, _cache8(k=FAKE + 8 * G, v=FAKE + 9 * G, ks=FAKE + 10 * G,
                                  vs=FAKE + 11 * G), **_apart8(scale=scale)) == N.ERR_INVALID_ARG
+
+
+def test_binding_before_init_refuses():
+    """The module by itself, without the library's entry points."""
+    code = ("import torch\n"
+            "from nvfp4_w4a4_quantized_08_b200 import _binding as b\n"
+            "z = lambda *s: torch.zeros(*s, dtype=torch.uint8)\n"
+            "try:\n"
+            "    b.gemv(torch.zeros(1, 32), z(8, 16), z(512), torch.zeros(1), 8, 32, 1,\n"
+            "           torch.float32, None, 0)\n"
+            "except RuntimeError as e:\n"
+            "    print(e)\n")
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                         cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert run.stdout.strip() == "init has not been called", run.stderr[-500:]
