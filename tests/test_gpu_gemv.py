@@ -240,3 +240,21 @@ def test_output_beside_x(orc, m):
         with pytest.raises(nv.NVFP4Error):
             nv.gemv(wide[:, 256:512], q, out=wide[:, at:at + 256])
     assert torch.equal(wide, before)
+
+
+@pytest.mark.parametrize("m,xd", [(1, torch.bfloat16), (5, torch.float32)])
+def test_offsets_past_32_bits(m, xd):
+    """Weights of more than 2^32 bytes of codes: the last rows."""
+    n, k = 620000, 14336
+    codes = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, device="cuda")
+    sf = torch.randint(0x30, 0x41, (nv.sf_bytes(n, k, nv.SF_ROWMAJOR),), dtype=torch.uint8,
+                       device="cuda")
+    q = nv.NVFP4Tensor(codes, sf, torch.full((1,), 2.0 ** -9, device="cuda"), n, k, nv.SF_ROWMAJOR)
+    assert codes.numel() > 2 ** 32
+    x = torch.randn(m, k, generator=torch.Generator().manual_seed(m)).to(xd).cuda()
+    y = nv.gemv(x, q, torch.float32)
+    for r in (slice(0, 40), slice(n - 200, n)):
+        c = codes[r].cpu().int()
+        v = E2M1[torch.stack((c & 15, c >> 4), 2).reshape(-1, k).long()]
+        s = sf.view(n, k // 16)[r].cpu().view(torch.float8_e4m3fn).double()
+        _check(y[:, r], x, v * s.repeat_interleave(16, 1) * 2.0 ** -9, False)

@@ -982,3 +982,13 @@ def test_a_chain_of_steps_in_one_graph(steps, batch, dim, hkv, hq, page, prompt)
         got, graph = run(lambda: None, captured)
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("batch,most", [(5000, 1), (700, 40)])
+def test_many_requests(batch, most):
+    """More requests than SMs by far, some without queries, some without tokens."""
+    r = random.Random(batch)
+    kv = [r.choice((0, 1, 16, 17, r.randint(1, 60))) for _ in range(batch)]
+    nq = [r.choice((0, 1, most)) for _ in range(batch)]
+    c = _random_cache(sum(-(-t // 16) for t in kv) + 2, 16, 1, 64, 31)
+    _attention_case(c, nq, kv, 2, True, 32, max_q=most)
