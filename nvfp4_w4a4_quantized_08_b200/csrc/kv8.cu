@@ -38,8 +38,8 @@ __device__ __forceinline__ int32_t pages_of(const Args& a, uint32_t n) {
 // Latency is all of it (a few hundred KB at most), so it is one launch: every CTA
 // computes the two prefix sums over the requests for itself (they are read from
 // L2; one request a thread up to 512) and then fills its share of the slot map
-// and the tables.  No CTA waits for another.  One request 2.5 us, 512 requests with 66
-// thousand new tokens 4.5 us: the launch, three loads in a row and the sums' barriers.
+// and the tables.  No CTA waits for another.  One request 2.3 us, 512 requests with 66
+// thousand new tokens 4.2 us: the launch, three loads in a row and the sums' barriers.
 __global__ void __launch_bounds__(kThreads) plan_kernel(const Args a) {
   extern __shared__ int32_t smem[];
   int32_t* cu = smem;                   // [batch + 1] tokens before each request
@@ -321,7 +321,7 @@ __device__ __forceinline__ uint32_t cluster_max(uint32_t v, uint32_t* buf, uint3
 //
 // 18 thousand tokens of 8 heads of 128 in 64-token pages (113 MB): 26 us, 66% of the copy rate
 // (one head a CTA 30 us: the latency of the slots in front of every 16 KB; 16-token pages of
-// 64 elements 21 us).  512 single tokens 11 us, 33 of them 3.4 us: two load latencies and
+// 64 elements 21 us).  512 single tokens 11 us, 33 of them 3.1 us: two load latencies and
 // the launch.  Pages of 880 tokens 69 us, 115 without the clusters.
 template <int kDim>
 __global__ void __launch_bounds__(kThreads, kResident) append_kernel(const Args a) {
